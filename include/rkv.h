@@ -40,11 +40,12 @@ extern "C" {
 #define RKV_OK 0
 #define RKV_ERR_ARG 1         /* bad pointer, size, layer index or alignment            */
 #define RKV_ERR_ORDER 2       /* start_frame != frames committed so far for that layer  */
-#define RKV_ERR_CAPACITY 3    /* n_frames > window_frames - sink_frames                 */
+#define RKV_ERR_CAPACITY 3    /* n_frames > window_frames - sink_frames; workspace too small */
 #define RKV_ERR_UNSUPPORTED 4 /* d != 128, window > 256 frames, time id beyond table    */
 #define RKV_ERR_CUDA 5        /* a CUDA runtime / driver call failed                    */
 #define RKV_ERR_TIMEOUT 6     /* a bounded device wait expired (read via poll)          */
 #define RKV_ERR_STATE 7       /* call needs rkv_set_rope_grid (or rkv_set_text_kv) first */
+#define RKV_ERR_PAGE 8        /* a length or page id on the device is out of bounds (read via poll) */
 
 #define RKV_ROPE_ABSOLUTE 0   /* time id = absolute frame index                         */
 #define RKV_ROPE_RELATIVE 1   /* time id re-based to the window and clamped to [0, W-1] */
@@ -328,6 +329,124 @@ typedef struct rkv_head_copy {
   int n_tok;
 } rkv_head_copy;
 int rkv_copy_heads(const rkv_head_copy* runs, int n_runs, int n_heads, void* stream);
+
+/* ------------------------------------------------------------------ paged caches
+ * Many streams of different length out of one pool of pages: a serving process that runs
+ * many sessions on one GPU keeps, per layer, K and V in pages of `page_tokens` tokens and
+ * gives every stream a list of pages, instead of one rolling window per handle. Queries may
+ * have more heads than K and V (grouped heads: query head h reads KV head
+ * h / (q_heads / kv_heads)), chunks have any number of tokens from one up, and eviction goes
+ * by the attention weight that each cached token gathered, beside sinks and recent tokens
+ * ([P1] §Attention Sink keeps the first tokens; [P2] §3 drops the oldest).
+ *
+ * These calls need no handle and allocate nothing. Lengths and page lists are DEVICE arrays,
+ * read when the kernels run, so a call captured into a CUDA graph follows what they hold at
+ * each replay; max_q and max_kv bound them on the host. Keys are cached as given (rotate them
+ * before the write); positions are places in the stream's page list.
+ *
+ * Every stream s has kv_len[s] cached tokens, its chunk's own included, and the chunk's n_q =
+ * q_start[s+1] - q_start[s] rows stand at places kv_len[s] - n_q .. kv_len[s] - 1. Streams
+ * without rows are left alone. Rows of the chunk tensors outside
+ * [q_start[0], q_start[n_seqs]) are neither read for a result nor written.
+ *
+ * What a device array holds is checked on the device: a length outside its bound (0 <=
+ * kv_len <= max_kv, 0 <= n_q <= max_q, row ranges inside the tensors) leaves that stream's
+ * outputs unwritten, a page id outside [0, n_pages) is never followed (its keys are read from
+ * page 0, writes to it are dropped), and both set `status`, read by rkv_paged_poll_status.
+ * Slots at and after kv_len may hold anything, NaN included; cached tokens before it have to
+ * be finite.
+ */
+
+/* The pages of one layer. page_stride: bf16 elements from one page to the next, a multiple of
+ *  8, at least kv_heads * page_tokens * 128 (more where K and V of a page lie side by side).
+ *  page_tokens is 16, 32, 64 or 128. k and v are 16-byte aligned device pointers. */
+typedef struct {
+  void* k;               /* [n_pages][kv_heads][page_tokens][128] bf16 */
+  void* v;               /* the same layout and page_stride            */
+  long long page_stride;
+  int n_pages;
+  int kv_heads;
+  int page_tokens;
+} rkv_page_pool;
+
+/* The streams of one step; every layer's calls of the step can share it. Device pointers
+ *  except where noted. table_stride * page_tokens must reach max_kv. */
+typedef struct {
+  const int* page_table; /* [n_seqs][table_stride]: page ids in logical order          */
+  const int* kv_len;     /* [n_seqs]                                                   */
+  const int* q_start;    /* [n_seqs + 1], not decreasing; may be NULL for rkv_paged_evict */
+  unsigned* status;      /* one word, zero at first; NULL: errors are not reported     */
+  int table_stride;      /* host value */
+  int n_seqs;            /* host value, at most 65536 */
+  int max_q;             /* host value: bound of every n_q    */
+  int max_kv;            /* host value: bound of every kv_len */
+} rkv_paged_batch;
+
+/*
+ * rkv_paged_write - the chunk's K and V into the pages: row i of stream s to place
+ *  kv_len[s] - n_q + i. A bit copy. k, v: [n_rows, kv_heads, 128] bf16, 16-byte aligned,
+ *  k_stride / v_stride elements from one row to the next (multiples of 8, at least
+ *  kv_heads * 128). A page listed twice under the written places holds one of the two writes.
+ *  Errors: RKV_ERR_ARG, RKV_ERR_UNSUPPORTED, RKV_ERR_CUDA.
+ */
+int rkv_paged_write(const rkv_page_pool* pool, const rkv_paged_batch* batch, const void* k, const void* v,
+                    int n_rows, long long k_stride, long long v_stride, void* stream);
+
+/*
+ * rkv_paged_attention - out = softmax(q K^T / sqrt(128)) V of every chunk row over its
+ *  stream's cached tokens: all of them (causal = 0: the tokens of a chunk see each other, as in
+ *  rkv_chunk_attention), or those up to its own place (causal = 1). A row that sees no token
+ *  (kv_len smaller than its chunk) gives zeros.
+ *  q, out: [n_rows, q_heads, 128] bf16, 16-byte aligned, row strides as above, not overlapping.
+ *  lse (may be NULL): [n_rows, q_heads] fp32, the natural log of the row's sum of exponentials
+ *  (-infinity for a row that sees nothing).
+ *  weight (may be NULL): [n_seqs][kv_heads][weight_stride] fp32, weight_stride >= max_kv: the
+ *  attention weight that this call's rows (all query heads of the KV head's group) gave to
+ *  each key is added to the key's entry, the entries of the chunk's own places starting from
+ *  zero. Entries at and after kv_len are left as they are. The sums are taken in a fixed
+ *  order: the same call gives the same bits.
+ *  workspace: rkv_paged_workspace bytes (no contents needed, nothing kept between calls),
+ *  16-byte aligned; calls that may overlap need workspaces of their own, and so do two
+ *  captured graphs that may.
+ *  Errors: RKV_ERR_ARG, RKV_ERR_CAPACITY (workspace too small), RKV_ERR_UNSUPPORTED
+ *  (page size, more than 128 query heads per KV head, sizes past the launch limits),
+ *  RKV_ERR_CUDA.
+ */
+int rkv_paged_attention(const rkv_page_pool* pool, const rkv_paged_batch* batch, const void* q, int q_heads,
+                        int n_rows, long long q_stride, void* out, long long out_stride, int causal, float* lse,
+                        float* weight, long long weight_stride, void* workspace, long long workspace_bytes,
+                        void* stream);
+
+/* rkv_paged_workspace - bytes of workspace that rkv_paged_attention needs for these host
+ *  values (device arrays are not read; it needs no GPU). with_weight: weight will be passed.
+ *  Errors: RKV_ERR_ARG, RKV_ERR_UNSUPPORTED. */
+int rkv_paged_workspace(const rkv_page_pool* pool, const rkv_paged_batch* batch, int q_heads, int n_rows,
+                        int with_weight, long long* bytes);
+
+/*
+ * rkv_paged_evict - trim every (stream, KV head) of one layer to at most `keep` tokens: the
+ *  first `sinks`, the last `recent`, and of the others those of largest weight (equal weights:
+ *  the earlier token; NaN ranks below everything), moved to the front of the stream's places
+ *  in their order: K, V and weight. Streams with kv_len <= keep stay as they are. The places
+ *  after the kept ones keep their old contents; pages that only hold such places can be freed
+ *  once every layer was trimmed. KV heads choose for themselves, so a place may hold different
+ *  tokens in different heads. No page may be in two places of the batch's lists.
+ *  weight: as in rkv_paged_attention. kept: [n_seqs][kv_heads][keep] int32, the old places of
+ *  the kept tokens, increasing, then -1. kv_len_out: [n_seqs] int32, min(kv_len, keep); it may
+ *  be batch->kv_len itself (then only in the last layer's call, since each layer needs the old
+ *  lengths).
+ *  A stream with a length outside its bound: kept all -1, kv_len_out 0.
+ *  Errors: RKV_ERR_ARG (keep < 1, sinks or recent < 0, sinks + recent > keep, pointers),
+ *  RKV_ERR_UNSUPPORTED, RKV_ERR_CUDA.
+ */
+int rkv_paged_evict(const rkv_page_pool* pool, const rkv_paged_batch* batch, float* weight,
+                    long long weight_stride, int keep, int sinks, int recent, int* kept, int* kv_len_out,
+                    void* stream);
+
+/* rkv_paged_poll_status - synchronise `stream`, read and clear the device word that
+ *  rkv_paged_batch names: RKV_ERR_TIMEOUT (a bounded wait expired), RKV_ERR_PAGE (a length or
+ *  page id out of bounds) or RKV_OK. Errors: RKV_ERR_ARG, RKV_ERR_CUDA. */
+int rkv_paged_poll_status(unsigned* status, void* stream);
 
 #ifdef __cplusplus
 }

@@ -24,6 +24,7 @@ ERR_UNSUPPORTED = 4
 ERR_CUDA = 5
 ERR_TIMEOUT = 6
 ERR_STATE = 7
+ERR_PAGE = 8
 
 ROPE_ABSOLUTE = 0
 ROPE_RELATIVE = 1
@@ -49,6 +50,20 @@ class HeadCopy(ctypes.Structure):
     _fields_ = [("src", _vp), ("dst", _vp), ("src_tok_stride", _c_ll), ("src_head_stride", _c_ll),
                 ("dst_tok_stride", _c_ll), ("dst_head_stride", _c_ll), ("n_tok", _c_int)]
 
+
+class _PagePool(ctypes.Structure):
+    """Mirror of ``rkv_page_pool``."""
+    _fields_ = [("k", _vp), ("v", _vp), ("page_stride", _c_ll), ("n_pages", _c_int), ("kv_heads", _c_int),
+                ("page_tokens", _c_int)]
+
+
+class _PagedBatch(ctypes.Structure):
+    """Mirror of ``rkv_paged_batch``."""
+    _fields_ = [("page_table", _vp), ("kv_len", _vp), ("q_start", _vp), ("status", _vp), ("table_stride", _c_int),
+                ("n_seqs", _c_int), ("max_q", _c_int), ("max_kv", _c_int)]
+
+
+_pool_p, _batch_p = ctypes.POINTER(_PagePool), ctypes.POINTER(_PagedBatch)
 
 _SIGS = {
     "rkv_create": ([_c_int] * 7 + [ctypes.POINTER(_vp)], _c_int),
@@ -77,6 +92,12 @@ _SIGS = {
     "rkv_timing_end": ([_vp, ctypes.POINTER(ctypes.c_float), _c_int, _int_p], _c_int),
     "rkv_plan_window": ([_c_int, _c_int, _c_int, _c_int, _c_int, _int_p, _c_int, _int_p], _c_int),
     "rkv_copy_heads": ([ctypes.POINTER(HeadCopy), _c_int, _c_int, _vp], _c_int),
+    "rkv_paged_write": ([_pool_p, _batch_p, _vp, _vp, _c_int, _c_ll, _c_ll, _vp], _c_int),
+    "rkv_paged_attention": ([_pool_p, _batch_p, _vp, _c_int, _c_int, _c_ll, _vp, _c_ll, _c_int, _vp, _vp, _c_ll,
+                             _vp, _c_ll, _vp], _c_int),
+    "rkv_paged_workspace": ([_pool_p, _batch_p, _c_int, _c_int, _c_int, ctypes.POINTER(_c_ll)], _c_int),
+    "rkv_paged_evict": ([_pool_p, _batch_p, _vp, _c_ll, _c_int, _c_int, _c_int, _vp, _vp, _vp], _c_int),
+    "rkv_paged_poll_status": ([_vp, _vp], _c_int),
 }
 for _name, (_args, _res) in _SIGS.items():
     try:
@@ -153,6 +174,154 @@ def flow_cfg_x0_renoise(xt, v_cond, v_uncond, eps, cfg_scale: float, sigma: floa
     _check(_lib.rkv_flow_cfg_x0_renoise(_ptr(xt), _ptr(v_cond), _ptr(v_uncond), _ptr(eps), float(cfg_scale),
                                         float(sigma), float(sigma_next), _ptr(x0_out), _ptr(xt_next_out),
                                         xt.numel(), _stream(stream)), "rkv_flow_cfg_x0_renoise")
+
+
+# ---------------------------------------------------------------------- paged caches
+def _expect(ok: bool, where: str) -> None:
+    if not ok:
+        raise RkvError(ERR_ARG, where)
+
+
+def _tensor(t, dtype: str, shape, where: str, device=None):
+    """Check type, device and shape (None: any extent) of a torch tensor argument."""
+    ok = str(t.dtype) == "torch." + dtype and t.is_cuda and len(t.shape) == len(shape)
+    ok = ok and all(want is None or have == want for have, want in zip(t.shape, shape))
+    _expect(ok and (device is None or t.device == device), where)
+    return t
+
+
+def _rows_tensor(t, heads: int, rows, device, where: str):
+    """A [rows, heads, 128] bf16 tensor whose rows may lie apart; returns the row stride."""
+    _tensor(t, "bfloat16", (rows, heads, 128), where, device)
+    rows, row, head, one = t.shape[0], *t.stride()
+    _expect(one == 1 and (head == 128 or heads == 1), where)
+    return row if rows > 1 else heads * 128
+
+
+def _launch(fn, where: str, device, stream, *args) -> None:
+    """Call with the tensors' device current and, unless one is given, its current stream."""
+    import torch
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    if torch.cuda.current_device() == device.index:
+        rc = fn(*args, _stream(stream))
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, _stream(stream))
+    _check(rc, where)
+
+
+class PagePool:
+    """One layer's pages: k and v, each [n_pages, kv_heads, page_tokens, 128] bf16, contiguous but for
+    the distance between pages, which is the same in both (two halves of one tensor will do)."""
+
+    def __init__(self, k, v):
+        where = "PagePool"
+        _tensor(k, "bfloat16", (None, None, None, 128), where)
+        _tensor(v, "bfloat16", k.shape, where, k.device)
+        n, h, p, _ = k.shape
+        for t in (k, v):
+            _expect(t.stride(3) == 1 and (p == 1 or t.stride(2) == 128) and (h == 1 or t.stride(1) == p * 128), where)
+        _expect(n == 1 or k.stride(0) == v.stride(0), where)
+        self.k, self.v, self.device, self.kv_heads = k, v, k.device, h
+        self._c = _PagePool(k.data_ptr(), v.data_ptr(), k.stride(0) if n > 1 else h * p * 128, n, h, p)
+
+
+class PagedBatch:
+    """The streams of one step: page_table [n_seqs, pages] int32, kv_len [n_seqs] int32, q_start
+    [n_seqs + 1] int32 (None for eviction only), all on the GPU, and host bounds of chunk rows and
+    cached tokens per stream. ``status``: one zeroed int32 on the GPU that collects errors
+    (``poll``); without it they are not reported. Layers can share one."""
+
+    def __init__(self, page_table, kv_len, q_start, max_q: int, max_kv: int, status=None):
+        where = "PagedBatch"
+        _tensor(page_table, "int32", (None, None), where)
+        n, width = page_table.shape
+        dev = page_table.device
+        _expect(page_table.stride(1) == 1 or width <= 1, where)
+        for t, shape in ((kv_len, (n,)), (q_start, (n + 1,)), (status, (1,))):
+            if t is not None:
+                _tensor(t, "int32", shape, where, dev)
+                _expect(t.is_contiguous(), where)
+        stride = page_table.stride(0) if n > 1 else width
+        _expect(stride >= width, where)
+        self.page_table, self.kv_len, self.q_start, self.status = page_table, kv_len, q_start, status
+        self.device, self.n_seqs = dev, n
+        self._c = _PagedBatch(_ptr(page_table), _ptr(kv_len), _ptr(q_start), _ptr(status), stride, n, max_q, max_kv)
+
+    def poll(self, stream=None) -> int:
+        """Synchronise the stream and return (and clear) the status: OK, ERR_PAGE or ERR_TIMEOUT."""
+        _expect(self.status is not None, "rkv_paged_poll_status")
+        import torch
+        with torch.cuda.device(self.device):
+            return _lib.rkv_paged_poll_status(_ptr(self.status), _stream(stream))
+
+
+def paged_write(pool: PagePool, batch: PagedBatch, k, v, stream=None) -> None:
+    """The chunk's K and V, [rows, kv_heads, 128] bf16, into the pages."""
+    where = "rkv_paged_write"
+    _expect(pool.device == batch.device, where)
+    ks = _rows_tensor(k, pool.kv_heads, None, pool.device, where)
+    vs = _rows_tensor(v, pool.kv_heads, k.shape[0], pool.device, where)
+    _launch(_lib.rkv_paged_write, where, pool.device, stream, pool._c, batch._c, k.data_ptr(), v.data_ptr(),
+            k.shape[0], ks, vs)
+
+
+def paged_workspace_bytes(pool: PagePool, batch: PagedBatch, rows: int, q_heads: int, weight: bool = False) -> int:
+    """Bytes of workspace that ``paged_attention`` needs for a chunk tensor of ``rows`` rows."""
+    n = _c_ll(0)
+    _check(_lib.rkv_paged_workspace(pool._c, batch._c, q_heads, rows, int(bool(weight)), ctypes.byref(n)),
+           "rkv_paged_workspace")
+    return n.value
+
+
+def paged_attention(pool: PagePool, batch: PagedBatch, q, out, causal: bool = True, lse=None, weight=None,
+                    workspace=None, stream=None) -> None:
+    """out = softmax(q K^T / sqrt(128)) V over each stream's pages; q, out [rows, q_heads, 128] bf16, lse
+    [rows, q_heads] fp32 (optional), weight [n_seqs, kv_heads, tokens] fp32 (optional): the attention weight
+    of every key, added up. ``workspace``: a uint8 tensor of ``paged_workspace_bytes`` (allocated on the
+    call's stream if None)."""
+    where = "rkv_paged_attention"
+    dev = pool.device
+    _expect(dev == batch.device and len(q.shape) == 3, where)
+    rows, heads = q.shape[0], q.shape[1]
+    qs = _rows_tensor(q, heads, None, dev, where)
+    os_ = _rows_tensor(out, heads, rows, dev, where)
+    if lse is not None:
+        _expect(_tensor(lse, "float32", (rows, heads), where, dev).is_contiguous(), where)
+    width = 0
+    if weight is not None:
+        _expect(_tensor(weight, "float32", (batch.n_seqs, pool.kv_heads, None), where, dev).is_contiguous(), where)
+        width = weight.shape[2]
+    if workspace is None:
+        import torch
+        size = paged_workspace_bytes(pool, batch, rows, heads, weight is not None)
+        if stream is None:
+            stream = torch.cuda.current_stream(dev)
+        elif isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, dev) if stream else torch.cuda.default_stream(dev)
+        with torch.cuda.stream(stream):
+            workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+    else:
+        _expect(_tensor(workspace, "uint8", (None,), where, dev).is_contiguous(), where)
+    _launch(_lib.rkv_paged_attention, where, dev, stream, pool._c, batch._c, q.data_ptr(), heads, rows, qs,
+            out.data_ptr(), os_, int(bool(causal)), _ptr(lse), _ptr(weight), width, workspace.data_ptr(),
+            workspace.shape[0])
+
+
+def paged_evict(pool: PagePool, batch: PagedBatch, weight, keep: int, sinks: int, recent: int, kept, kv_len_out,
+                stream=None) -> None:
+    """Trim every (stream, KV head) to its first ``sinks``, last ``recent`` and heaviest other tokens, ``keep``
+    in all, in their order. weight [n_seqs, kv_heads, tokens] fp32, kept [n_seqs, kv_heads, keep] int32 and
+    kv_len_out [n_seqs] int32 (both written)."""
+    where = "rkv_paged_evict"
+    dev, n = pool.device, batch.n_seqs
+    _expect(dev == batch.device, where)
+    for t, dtype, shape in ((weight, "float32", (n, pool.kv_heads, None)), (kept, "int32", (n, pool.kv_heads, keep)),
+                            (kv_len_out, "int32", (n,))):
+        _expect(_tensor(t, dtype, shape, where, dev).is_contiguous(), where)
+    _launch(_lib.rkv_paged_evict, where, dev, stream, pool._c, batch._c, weight.data_ptr(), weight.shape[2], keep,
+            sinks, recent, kept.data_ptr(), kv_len_out.data_ptr())
 
 
 class RollingKV:

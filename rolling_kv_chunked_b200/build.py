@@ -25,9 +25,9 @@ ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 LIB = os.path.join(HERE, "librkv.so")
 SYNTH_LIB = os.path.join(ROOT, "synth", "libsynth.so")
 
-CU_SOURCES = ["rkv_kernels.cu", "rkv_attention.cu", "rkv_noalloc.cu"]
-CPP_SOURCES = ["rkv_host.cpp"]
-HEADERS = ["ptx_sm100.cuh", "numeric.cuh", "rkv_internal.h"]
+CU_SOURCES = ["rkv_kernels.cu", "rkv_attention.cu", "rkv_noalloc.cu", "rkv_paged.cu", "rkv_paged_attention.cu"]
+CPP_SOURCES = ["rkv_host.cpp", "rkv_paged_host.cpp"]
+HEADERS = ["ptx_sm100.cuh", "numeric.cuh", "paged.cuh", "rkv_internal.h"]
 
 
 def _run(cmd, verbose):

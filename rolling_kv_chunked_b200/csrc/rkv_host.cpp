@@ -906,10 +906,11 @@ RKV_API const char* rkv_status_string(int status) {
     case RKV_OK: return "ok";
     case RKV_ERR_ARG: return "invalid argument";
     case RKV_ERR_ORDER: return "start_frame does not follow the frames committed so far";
-    case RKV_ERR_CAPACITY: return "chunk larger than window_frames - sink_frames";
+    case RKV_ERR_CAPACITY: return "chunk larger than window_frames - sink_frames, or workspace too small";
     case RKV_ERR_UNSUPPORTED: return "unsupported size (d != 128, window > 256 frames or time id beyond table)";
     case RKV_ERR_CUDA: return "CUDA runtime or driver error";
     case RKV_ERR_TIMEOUT: return "a bounded device wait expired";
+    case RKV_ERR_PAGE: return "a paged cache's length or page id is out of bounds";
     case RKV_ERR_STATE: return "required state not set (rkv_set_rope_grid, or rkv_set_text_kv for cross-attention)";
     default: return "unknown status";
   }

@@ -20,6 +20,8 @@ constexpr int kTimeTable = 65536;  // time ids in [0, kTimeTable) have cos/sin r
 
 // Device status word bits.
 constexpr unsigned kStatusTimeout = 1u;
+constexpr unsigned kStatusPage = 2u;    // a page id outside the pool
+constexpr unsigned kStatusLength = 4u;  // a length or row range outside its bound
 
 // ---------------------------------------------------------------- frame runs
 // A run is a contiguous block of n_tok tokens copied (and optionally rotated)
@@ -114,5 +116,51 @@ constexpr int kPartRow = 132;  // floats per partial row: 128 of O, the referenc
 cudaError_t launch_attention(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_vc,
                              const CUtensorMap& tm_vn, const CUtensorMap& tm_o, const AttnParams& p,
                              cudaStream_t stream);
+
+// ---------------------------------------------------------------- paged caches
+// What every paged kernel needs of the pool and the batch (include/rkv.h, rkv_page_pool and
+// rkv_paged_batch).
+struct PagedView {
+  uint16_t* k;
+  uint16_t* v;
+  long long page_stride;
+  const int* table;
+  const int* kv_len;
+  const int* q_start;
+  unsigned* status;
+  int n_pages, kv_heads, page_shift;  // page_tokens = 1 << page_shift
+  int table_stride, n_seqs, n_rows, max_q, max_kv;
+};
+
+struct PagedWriteParams {
+  PagedView view;
+  const uint16_t* k;
+  const uint16_t* v;
+  long long k_stride, v_stride;
+};
+
+struct PagedAttnParams {
+  PagedView view;
+  const uint16_t* q;
+  uint16_t* out;
+  float* lse;     // [n_rows][q_heads], natural log; null: not wanted
+  float* weight;  // [n_seqs][kv_heads][weight_stride]; null: not wanted
+  long long q_stride, out_stride, weight_stride;
+  int q_heads, group, causal;
+  float scale_log2;  // log2(e) / sqrt(d)
+};
+
+struct PagedEvictParams {
+  PagedView view;
+  float* weight;
+  long long weight_stride;
+  int keep, sinks, recent;
+  int* kept;
+  int* kv_len_out;
+};
+
+cudaError_t launch_paged_write(const PagedWriteParams& p, cudaStream_t stream);
+cudaError_t launch_paged_attention(const PagedAttnParams& p, float* lse2, cudaStream_t stream);
+cudaError_t launch_paged_evict(const PagedEvictParams& p, cudaStream_t stream);
 
 }  // namespace rkv

@@ -1,0 +1,189 @@
+// Host side of the paged caches: argument checks and launches. Every exported function is
+// declared and documented in include/rkv.h.
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include "../../include/rkv.h"
+#include "rkv_internal.h"
+
+#define RKV_API extern "C" __attribute__((visibility("default")))
+
+using rkv::kHeadDim;
+using rkv::PagedView;
+
+namespace {
+
+constexpr int kMaxSeqs = 1 << 16;
+constexpr int kMaxGroup = 128;  // query heads of one KV head: one tile of query rows holds a token's
+
+bool aligned16(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+int cuda_rc(cudaError_t e) { return e == cudaSuccess ? RKV_OK : RKV_ERR_CUDA; }
+
+// Host values of the pool and the batch (what rkv_paged_workspace looks at, no pointers).
+int check_sizes(const rkv_page_pool* pool, const rkv_paged_batch* b, int n_rows) {
+  if (pool == nullptr || b == nullptr || n_rows < 0) return RKV_ERR_ARG;
+  if (pool->n_pages < 1 || pool->kv_heads < 1 || pool->page_tokens < 1 || b->n_seqs < 0 || b->max_q < 0 ||
+      b->max_kv < 0 || b->table_stride < 0)
+    return RKV_ERR_ARG;
+  const int p = pool->page_tokens;
+  if (p != 16 && p != 32 && p != 64 && p != 128) return RKV_ERR_UNSUPPORTED;
+  const long long page = static_cast<long long>(pool->kv_heads) * p * kHeadDim;
+  if (pool->page_stride < page || pool->page_stride % 8 != 0) return RKV_ERR_ARG;
+  if (static_cast<long long>(b->table_stride) * p < b->max_kv) return RKV_ERR_ARG;
+  // a tensor map's stride and extents; the launch grids
+  if (pool->page_stride >= (1LL << 38) || static_cast<long long>(pool->kv_heads) * p >= (1LL << 31) ||
+      b->n_seqs > kMaxSeqs || static_cast<long long>(b->n_seqs) * pool->kv_heads >= (1LL << 24) ||
+      b->max_kv > (1 << 30))
+    return RKV_ERR_UNSUPPORTED;
+  return RKV_OK;
+}
+
+int check_batch(const rkv_page_pool* pool, const rkv_paged_batch* b, int n_rows, bool rows) {
+  const int rc = check_sizes(pool, b, n_rows);
+  if (rc) return rc;
+  if (!aligned16(pool->k) || !aligned16(pool->v)) return RKV_ERR_ARG;
+  if (b->status != nullptr && !aligned4(b->status)) return RKV_ERR_ARG;
+  if (b->n_seqs > 0 && (!aligned4(b->page_table) || !aligned4(b->kv_len))) return RKV_ERR_ARG;
+  if (b->n_seqs > 0 && rows && !aligned4(b->q_start)) return RKV_ERR_ARG;
+  return RKV_OK;
+}
+
+bool row_stride_ok(long long stride, int heads) {
+  return stride % 8 == 0 && stride >= static_cast<long long>(heads) * kHeadDim && stride < (1LL << 38);
+}
+
+PagedView view_of(const rkv_page_pool* pool, const rkv_paged_batch* b, int n_rows) {
+  PagedView w;
+  std::memset(&w, 0, sizeof(w));
+  w.k = static_cast<uint16_t*>(pool->k);
+  w.v = static_cast<uint16_t*>(pool->v);
+  w.page_stride = pool->page_stride;
+  w.n_pages = pool->n_pages;
+  w.kv_heads = pool->kv_heads;
+  while ((1 << w.page_shift) < pool->page_tokens) ++w.page_shift;
+  w.table = b->page_table;
+  w.kv_len = b->kv_len;
+  w.q_start = b->q_start;
+  w.status = b->status;
+  w.table_stride = b->table_stride;
+  w.n_seqs = b->n_seqs;
+  w.n_rows = n_rows;
+  w.max_q = b->max_q;
+  w.max_kv = b->max_kv;
+  return w;
+}
+
+int check_heads(const rkv_page_pool* pool, int q_heads) {
+  if (q_heads < 1 || q_heads % pool->kv_heads != 0) return RKV_ERR_ARG;
+  if (q_heads / pool->kv_heads > kMaxGroup) return RKV_ERR_UNSUPPORTED;
+  return RKV_OK;
+}
+
+// whether two row tensors of n rows share a byte range
+bool overlap(const void* a, long long stride_a, const void* b, long long stride_b, int n, int heads) {
+  const long long row = static_cast<long long>(heads) * kHeadDim;
+  const char* a0 = static_cast<const char*>(a);
+  const char* b0 = static_cast<const char*>(b);
+  return a0 < b0 + 2 * ((n - 1) * stride_b + row) && b0 < a0 + 2 * ((n - 1) * stride_a + row);
+}
+
+}  // namespace
+
+RKV_API int rkv_paged_write(const rkv_page_pool* pool, const rkv_paged_batch* batch, const void* k, const void* v,
+                            int n_rows, long long k_stride, long long v_stride, void* stream) {
+  const int rc = check_batch(pool, batch, n_rows, true);
+  if (rc) return rc;
+  if (n_rows == 0 || batch->n_seqs == 0) return RKV_OK;
+  if (!aligned16(k) || !aligned16(v) || !row_stride_ok(k_stride, pool->kv_heads) ||
+      !row_stride_ok(v_stride, pool->kv_heads))
+    return RKV_ERR_ARG;
+  rkv::PagedWriteParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.view = view_of(pool, batch, n_rows);
+  p.k = static_cast<const uint16_t*>(k);
+  p.v = static_cast<const uint16_t*>(v);
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  return cuda_rc(rkv::launch_paged_write(p, static_cast<cudaStream_t>(stream)));
+}
+
+RKV_API int rkv_paged_workspace(const rkv_page_pool* pool, const rkv_paged_batch* batch, int q_heads, int n_rows,
+                                int with_weight, long long* bytes) {
+  int rc = check_sizes(pool, batch, n_rows);
+  if (rc) return rc;
+  if (bytes == nullptr) return RKV_ERR_ARG;
+  rc = check_heads(pool, q_heads);
+  if (rc) return rc;
+  *bytes = with_weight ? 4LL * n_rows * q_heads : 0;
+  return RKV_OK;
+}
+
+RKV_API int rkv_paged_attention(const rkv_page_pool* pool, const rkv_paged_batch* batch, const void* q, int q_heads,
+                                int n_rows, long long q_stride, void* out, long long out_stride, int causal,
+                                float* lse, float* weight, long long weight_stride, void* workspace,
+                                long long workspace_bytes, void* stream) {
+  int rc = check_batch(pool, batch, n_rows, true);
+  if (rc) return rc;
+  rc = check_heads(pool, q_heads);
+  if (rc) return rc;
+  if (lse != nullptr && !aligned4(lse)) return RKV_ERR_ARG;
+  if (weight != nullptr && (!aligned4(weight) || weight_stride < batch->max_kv)) return RKV_ERR_ARG;
+  if (n_rows == 0 || batch->n_seqs == 0) return RKV_OK;
+  if (!aligned16(q) || !aligned16(out) || !row_stride_ok(q_stride, q_heads) || !row_stride_ok(out_stride, q_heads) ||
+      overlap(q, q_stride, out, out_stride, n_rows, q_heads))
+    return RKV_ERR_ARG;
+  long long need = 0;
+  rc = rkv_paged_workspace(pool, batch, q_heads, n_rows, weight != nullptr, &need);
+  if (rc) return rc;
+  if (workspace_bytes < need) return RKV_ERR_CAPACITY;
+  if (need > 0 && !aligned16(workspace)) return RKV_ERR_ARG;
+  rkv::PagedAttnParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.view = view_of(pool, batch, n_rows);
+  p.q = static_cast<const uint16_t*>(q);
+  p.out = static_cast<uint16_t*>(out);
+  p.lse = lse;
+  p.weight = weight;
+  p.q_stride = q_stride;
+  p.out_stride = out_stride;
+  p.weight_stride = weight_stride;
+  p.q_heads = q_heads;
+  p.group = q_heads / pool->kv_heads;
+  p.causal = causal != 0;
+  p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(kHeadDim)));
+  return cuda_rc(rkv::launch_paged_attention(p, static_cast<float*>(workspace), static_cast<cudaStream_t>(stream)));
+}
+
+RKV_API int rkv_paged_evict(const rkv_page_pool* pool, const rkv_paged_batch* batch, float* weight,
+                            long long weight_stride, int keep, int sinks, int recent, int* kept, int* kv_len_out,
+                            void* stream) {
+  const int rc = check_batch(pool, batch, 0, false);
+  if (rc) return rc;
+  if (keep < 1 || sinks < 0 || recent < 0 || static_cast<long long>(sinks) + recent > keep) return RKV_ERR_ARG;
+  if (batch->n_seqs == 0) return RKV_OK;
+  if (!aligned4(weight) || weight_stride < batch->max_kv || !aligned4(kept) || !aligned4(kv_len_out))
+    return RKV_ERR_ARG;
+  rkv::PagedEvictParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.view = view_of(pool, batch, 0);
+  p.weight = weight;
+  p.weight_stride = weight_stride;
+  p.keep = keep;
+  p.sinks = sinks;
+  p.recent = recent;
+  p.kept = kept;
+  p.kv_len_out = kv_len_out;
+  return cuda_rc(rkv::launch_paged_evict(p, static_cast<cudaStream_t>(stream)));
+}
+
+RKV_API int rkv_paged_poll_status(unsigned* status, void* stream) {
+  if (!aligned4(status)) return RKV_ERR_ARG;
+  if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return RKV_ERR_CUDA;
+  unsigned word = 0;
+  if (cudaMemcpy(&word, status, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess) return RKV_ERR_CUDA;
+  if (word != 0 && cudaMemset(status, 0, sizeof(word)) != cudaSuccess) return RKV_ERR_CUDA;
+  if (word & rkv::kStatusTimeout) return RKV_ERR_TIMEOUT;
+  return (word & (rkv::kStatusPage | rkv::kStatusLength)) ? RKV_ERR_PAGE : RKV_OK;
+}
