@@ -99,8 +99,10 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
+}  // namespace
+
 // 3D bf16 map, innermost dimension d = 128 elements, box {64, box1, box2}, 128-byte swizzle.
-bool encode_map(CUtensorMap* m, const void* base, uint64_t dim1, uint64_t dim2, uint64_t stride1_bytes,
+bool rkv::encode_map(CUtensorMap* m, const void* base, uint64_t dim1, uint64_t dim2, uint64_t stride1_bytes,
                 uint64_t stride2_bytes, uint32_t box1, uint32_t box2) {
   auto fn = encode_fn();
   if (!fn) return false;
@@ -113,6 +115,10 @@ bool encode_map(CUtensorMap* m, const void* base, uint64_t dim1, uint64_t dim2, 
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
+
+namespace {
+
+using rkv::encode_map;
 
 // head-major [H][rows][d], boxes of box_rows rows of one head
 bool encode_head_major(CUtensorMap* m, const void* base, int rows, int H, int box_rows) {

@@ -23,6 +23,11 @@ constexpr unsigned kStatusTimeout = 1u;
 constexpr unsigned kStatusPage = 2u;    // a page id outside the pool
 constexpr unsigned kStatusLength = 4u;  // a length or row range outside its bound
 
+// 3D bf16 tensor map, innermost dimension d = 128 elements, box {64, box1, box2}, 128-byte swizzle
+// (rkv_host.cpp).
+bool encode_map(CUtensorMap* m, const void* base, uint64_t dim1, uint64_t dim2, uint64_t stride1_bytes,
+                uint64_t stride2_bytes, uint32_t box1, uint32_t box2);
+
 // ---------------------------------------------------------------- frame runs
 // A run is a contiguous block of n_tok tokens copied (and optionally rotated)
 // from src to dst. Element (token t, head h, dim c) lives at
@@ -139,6 +144,18 @@ struct PagedWriteParams {
   long long k_stride, v_stride;
 };
 
+// How a call is cut up (a host rule on the batch's host values; workspace offsets in bytes).
+struct PagedPlan {
+  int rows_form;     // 1: at most kPagedRows rows per stream and KV head, the form for single tokens
+  int block_tokens;  // chunk tokens of one block of rows
+  int split_keys;    // cached tokens per part of a block's key stream
+  int n_split;       // parts at most
+  long long lse, part, part_ml, total;  // -1: not used
+};
+
+constexpr int kPagedRows = 16;
+constexpr int kPagedMaxSplit = 256;
+
 struct PagedAttnParams {
   PagedView view;
   const uint16_t* q;
@@ -148,6 +165,12 @@ struct PagedAttnParams {
   long long q_stride, out_stride, weight_stride;
   int q_heads, group, causal;
   float scale_log2;  // log2(e) / sqrt(d)
+  // workspace
+  float* lse2;      // [n_rows][q_heads], log2; null when no weight is wanted
+  float* part;      // [n_split][n_rows][q_heads][128]: unnormalised sums of p v
+  float2* part_ml;  // [n_split][n_rows][q_heads]: reference (log2) and sum of p
+  int block_tokens, split_keys, n_split;
+  unsigned long long wait_limit_ns;
 };
 
 struct PagedEvictParams {
@@ -160,7 +183,13 @@ struct PagedEvictParams {
 };
 
 cudaError_t launch_paged_write(const PagedWriteParams& p, cudaStream_t stream);
-cudaError_t launch_paged_attention(const PagedAttnParams& p, float* lse2, cudaStream_t stream);
+// tm_k, tm_v: boxes of min(page_tokens, kPagedDecodeTile) tokens, 64 columns.
+constexpr int kPagedDecodeTile = 64;
+cudaError_t launch_paged_decode(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const PagedAttnParams& p,
+                                cudaStream_t stream);
+cudaError_t launch_paged_attention(const PagedAttnParams& p, cudaStream_t stream);
+cudaError_t launch_paged_combine(const PagedAttnParams& p, cudaStream_t stream);
+cudaError_t launch_paged_weight(const PagedAttnParams& p, cudaStream_t stream);
 cudaError_t launch_paged_evict(const PagedEvictParams& p, cudaStream_t stream);
 
 }  // namespace rkv

@@ -10,7 +10,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 
 // One warp per (chunk row, query head), four elements of d per lane, one key at a time with a
 // running maximum and sum.
-__global__ void __launch_bounds__(128) paged_attention_kernel(const __grid_constant__ PagedAttnParams p, float* lse2) {
+__global__ void __launch_bounds__(128) paged_attention_kernel(const __grid_constant__ PagedAttnParams p) {
   const PagedView& w = p.view;
   const long long gw = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
   const int row = static_cast<int>(gw / p.q_heads), head = static_cast<int>(gw % p.q_heads);
@@ -55,13 +55,12 @@ __global__ void __launch_bounds__(128) paged_attention_kernel(const __grid_const
   if (lane == 0) {
     const float z = l > 0.f ? m + log2f(l) : -INFINITY;
     if (p.lse != nullptr) p.lse[static_cast<long long>(row) * p.q_heads + head] = z * kLn2;
-    if (lse2 != nullptr) lse2[static_cast<long long>(row) * p.q_heads + head] = z;
+    if (p.lse2 != nullptr) p.lse2[static_cast<long long>(row) * p.q_heads + head] = z;
   }
 }
 
 // One warp per (stream, KV head, key): the key's weight over the rows that see it.
-__global__ void __launch_bounds__(128) paged_weight_kernel(const __grid_constant__ PagedAttnParams p,
-                                                           const float* lse2) {
+__global__ void __launch_bounds__(128) paged_weight_kernel(const __grid_constant__ PagedAttnParams p) {
   const PagedView& w = p.view;
   const int j = blockIdx.x * 4 + (threadIdx.x >> 5);
   const int s = blockIdx.y / w.kv_heads, h = blockIdx.y % w.kv_heads;
@@ -82,7 +81,7 @@ __global__ void __launch_bounds__(128) paged_weight_kernel(const __grid_constant
       float x = k0 * bf16_to_f32(qx.x & 0xffff) + k1 * bf16_to_f32(qx.x >> 16) + k2 * bf16_to_f32(qx.y & 0xffff) +
                 k3 * bf16_to_f32(qx.y >> 16);
       for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-      sum += exp2f(x * p.scale_log2 - lse2[row * p.q_heads + head]);
+      sum += exp2f(x * p.scale_log2 - p.lse2[row * p.q_heads + head]);
     }
   if (lane == 0) {
     float* to = p.weight + (static_cast<long long>(s) * w.kv_heads + h) * p.weight_stride + j;
@@ -92,12 +91,14 @@ __global__ void __launch_bounds__(128) paged_weight_kernel(const __grid_constant
 
 }  // namespace
 
-cudaError_t launch_paged_attention(const PagedAttnParams& p, float* lse2, cudaStream_t stream) {
+cudaError_t launch_paged_attention(const PagedAttnParams& p, cudaStream_t stream) {
   const long long warps = static_cast<long long>(p.view.n_rows) * p.q_heads;
-  paged_attention_kernel<<<static_cast<unsigned>((warps + 3) / 4), 128, 0, stream>>>(p, lse2);
-  cudaError_t err = cudaGetLastError();
-  if (err != cudaSuccess || p.weight == nullptr) return err;
-  paged_weight_kernel<<<dim3((p.view.max_kv + 3) / 4, p.view.n_seqs * p.view.kv_heads), 128, 0, stream>>>(p, lse2);
+  paged_attention_kernel<<<static_cast<unsigned>((warps + 3) / 4), 128, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_paged_weight(const PagedAttnParams& p, cudaStream_t stream) {
+  paged_weight_kernel<<<dim3((p.view.max_kv + 3) / 4, p.view.n_seqs * p.view.kv_heads), 128, 0, stream>>>(p);
   return cudaGetLastError();
 }
 

@@ -1,5 +1,6 @@
 // Host side of the paged caches: argument checks and launches. Every exported function is
 // declared and documented in include/rkv.h.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -15,6 +16,7 @@ using rkv::PagedView;
 namespace {
 
 constexpr int kMaxSeqs = 1 << 16;
+constexpr unsigned long long kWaitNs = 2000000000ull;  // cap on each device wait
 constexpr int kMaxGroup = 128;  // query heads of one KV head: one tile of query rows holds a token's
 
 bool aligned16(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -75,10 +77,55 @@ PagedView view_of(const rkv_page_pool* pool, const rkv_paged_batch* b, int n_row
   return w;
 }
 
-int check_heads(const rkv_page_pool* pool, int q_heads) {
+int check_heads(const rkv_page_pool* pool, int q_heads, int n_rows) {
   if (q_heads < 1 || q_heads % pool->kv_heads != 0) return RKV_ERR_ARG;
-  if (q_heads / pool->kv_heads > kMaxGroup) return RKV_ERR_UNSUPPORTED;
+  if (q_heads / pool->kv_heads > kMaxGroup || static_cast<long long>(n_rows) * q_heads >= (1LL << 31))
+    return RKV_ERR_UNSUPPORTED;
   return RKV_OK;
+}
+
+// How the call is cut up. Blocks of the single-token form take one (stream, KV head) each, two to an
+// SM; a key stream is split so that the batch, were every stream max_kv long, would give each SM's
+// two places four blocks (shorter streams then give fewer, never idle ones), but no shorter than
+// kMinSplit tokens, below which a block's fixed cost outweighs its share.
+constexpr int kSms = 148;
+constexpr int kMinSplit = 256;
+
+rkv::PagedPlan plan_of(const rkv_page_pool* pool, const rkv_paged_batch* b, int q_heads, int n_rows, bool weight) {
+  rkv::PagedPlan p;
+  std::memset(&p, 0, sizeof(p));
+  const int group = q_heads / pool->kv_heads;
+  p.rows_form = static_cast<long long>(b->max_q) * group <= rkv::kPagedRows;
+  p.block_tokens = b->max_q > 0 ? b->max_q : 1;
+  p.n_split = 1;
+  p.split_keys = b->max_kv > 0 ? b->max_kv : 1;
+  if (p.rows_form) {
+    const long long blocks = static_cast<long long>(b->n_seqs) * pool->kv_heads;
+    const long long want = 8LL * kSms;
+    long long len = (b->max_kv * blocks + want - 1) / want;
+    len = std::max<long long>(len, kMinSplit);
+    len = std::max<long long>(len, (b->max_kv + rkv::kPagedMaxSplit - 1) / rkv::kPagedMaxSplit);
+    len = (len + rkv::kPagedDecodeTile - 1) / rkv::kPagedDecodeTile * rkv::kPagedDecodeTile;
+    p.split_keys = static_cast<int>(len);
+    p.n_split = std::max(1, static_cast<int>((b->max_kv + len - 1) / len));
+  }
+  const long long heads = static_cast<long long>(n_rows) * q_heads;
+  auto take = [&p](long long bytes) {
+    const long long at = p.total;
+    p.total += (bytes + 255) / 256 * 256;
+    return at;
+  };
+  p.lse = weight ? take(4 * heads) : -1;
+  p.part = p.n_split > 1 ? take(4 * heads * kHeadDim * p.n_split) : -1;
+  p.part_ml = p.n_split > 1 ? take(8 * heads * p.n_split) : -1;
+  return p;
+}
+
+// The pages as a tensor of 64-column boxes of min(page_tokens, tile) tokens.
+bool encode_pages(CUtensorMap* m, const void* base, const rkv_page_pool* pool, int tile) {
+  return rkv::encode_map(m, base, static_cast<uint64_t>(pool->kv_heads) * pool->page_tokens, pool->n_pages,
+                         kHeadDim * 2, static_cast<uint64_t>(pool->page_stride) * 2,
+                         std::min(pool->page_tokens, tile), 1);
 }
 
 // whether two row tensors of n rows share a byte range
@@ -114,9 +161,9 @@ RKV_API int rkv_paged_workspace(const rkv_page_pool* pool, const rkv_paged_batch
   int rc = check_sizes(pool, batch, n_rows);
   if (rc) return rc;
   if (bytes == nullptr) return RKV_ERR_ARG;
-  rc = check_heads(pool, q_heads);
+  rc = check_heads(pool, q_heads, n_rows);
   if (rc) return rc;
-  *bytes = with_weight ? 4LL * n_rows * q_heads : 0;
+  *bytes = plan_of(pool, batch, q_heads, n_rows, with_weight != 0).total;
   return RKV_OK;
 }
 
@@ -126,7 +173,7 @@ RKV_API int rkv_paged_attention(const rkv_page_pool* pool, const rkv_paged_batch
                                 long long workspace_bytes, void* stream) {
   int rc = check_batch(pool, batch, n_rows, true);
   if (rc) return rc;
-  rc = check_heads(pool, q_heads);
+  rc = check_heads(pool, q_heads, n_rows);
   if (rc) return rc;
   if (lse != nullptr && !aligned4(lse)) return RKV_ERR_ARG;
   if (weight != nullptr && (!aligned4(weight) || weight_stride < batch->max_kv)) return RKV_ERR_ARG;
@@ -134,11 +181,9 @@ RKV_API int rkv_paged_attention(const rkv_page_pool* pool, const rkv_paged_batch
   if (!aligned16(q) || !aligned16(out) || !row_stride_ok(q_stride, q_heads) || !row_stride_ok(out_stride, q_heads) ||
       overlap(q, q_stride, out, out_stride, n_rows, q_heads))
     return RKV_ERR_ARG;
-  long long need = 0;
-  rc = rkv_paged_workspace(pool, batch, q_heads, n_rows, weight != nullptr, &need);
-  if (rc) return rc;
-  if (workspace_bytes < need) return RKV_ERR_CAPACITY;
-  if (need > 0 && !aligned16(workspace)) return RKV_ERR_ARG;
+  const rkv::PagedPlan plan = plan_of(pool, batch, q_heads, n_rows, weight != nullptr);
+  if (workspace_bytes < plan.total) return RKV_ERR_CAPACITY;
+  if (plan.total > 0 && !aligned16(workspace)) return RKV_ERR_ARG;
   rkv::PagedAttnParams p;
   std::memset(&p, 0, sizeof(p));
   p.view = view_of(pool, batch, n_rows);
@@ -153,7 +198,28 @@ RKV_API int rkv_paged_attention(const rkv_page_pool* pool, const rkv_paged_batch
   p.group = q_heads / pool->kv_heads;
   p.causal = causal != 0;
   p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(kHeadDim)));
-  return cuda_rc(rkv::launch_paged_attention(p, static_cast<float*>(workspace), static_cast<cudaStream_t>(stream)));
+  char* ws = static_cast<char*>(workspace);
+  if (plan.lse >= 0) p.lse2 = reinterpret_cast<float*>(ws + plan.lse);
+  if (plan.part >= 0) p.part = reinterpret_cast<float*>(ws + plan.part);
+  if (plan.part_ml >= 0) p.part_ml = reinterpret_cast<float2*>(ws + plan.part_ml);
+  p.block_tokens = plan.block_tokens;
+  p.split_keys = plan.split_keys;
+  p.n_split = plan.n_split;
+  p.wait_limit_ns = kWaitNs;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t err;
+  if (plan.rows_form) {
+    CUtensorMap tm_k, tm_v;
+    if (!encode_pages(&tm_k, pool->k, pool, rkv::kPagedDecodeTile) ||
+        !encode_pages(&tm_v, pool->v, pool, rkv::kPagedDecodeTile))
+      return RKV_ERR_CUDA;
+    err = rkv::launch_paged_decode(tm_k, tm_v, p, st);
+  } else {
+    err = rkv::launch_paged_attention(p, st);
+  }
+  if (err == cudaSuccess && plan.n_split > 1) err = rkv::launch_paged_combine(p, st);
+  if (err == cudaSuccess && weight != nullptr) err = rkv::launch_paged_weight(p, st);
+  return cuda_rc(err);
 }
 
 RKV_API int rkv_paged_evict(const rkv_page_pool* pool, const rkv_paged_batch* batch, float* weight,
