@@ -150,7 +150,9 @@ struct PagedPlan {
   int block_tokens;  // chunk tokens of one block of rows
   int split_keys;    // cached tokens per part of a block's key stream
   int n_split;       // parts at most
-  long long lse, part, part_ml, total;  // -1: not used
+  int n_blocks;      // blocks of chunk tokens in the batch at most
+  long long lse, part, part_ml, scores, total;  // -1: not used
+  long long score_stride;
 };
 
 constexpr int kPagedRows = 16;
@@ -169,7 +171,9 @@ struct PagedAttnParams {
   float* lse2;      // [n_rows][q_heads], log2; null when no weight is wanted
   float* part;      // [n_split][n_rows][q_heads][128]: unnormalised sums of p v
   float2* part_ml;  // [n_split][n_rows][q_heads]: reference (log2) and sum of p
-  int block_tokens, split_keys, n_split;
+  float* scores;    // [n_rows][q_heads][score_stride]: log2 scores of the single-token form; null: not kept
+  long long score_stride;
+  int block_tokens, n_blocks, split_keys, n_split;
   unsigned long long wait_limit_ns;
 };
 
@@ -187,9 +191,14 @@ cudaError_t launch_paged_write(const PagedWriteParams& p, cudaStream_t stream);
 constexpr int kPagedDecodeTile = 64;
 cudaError_t launch_paged_decode(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const PagedAttnParams& p,
                                 cudaStream_t stream);
-cudaError_t launch_paged_attention(const PagedAttnParams& p, cudaStream_t stream);
+// tm_q: boxes of 64 columns, the group's heads and floor(128 / group) tokens; tm_k, tm_v: boxes of
+// min(page_tokens, kKeyBox) tokens.
+cudaError_t launch_paged_chunk(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                               const PagedAttnParams& p, cudaStream_t stream);
 cudaError_t launch_paged_combine(const PagedAttnParams& p, cudaStream_t stream);
-cudaError_t launch_paged_weight(const PagedAttnParams& p, cudaStream_t stream);
+cudaError_t launch_paged_weight(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const PagedAttnParams& p,
+                                cudaStream_t stream);
+cudaError_t launch_paged_token_weight(const PagedAttnParams& p, cudaStream_t stream);
 cudaError_t launch_paged_evict(const PagedEvictParams& p, cudaStream_t stream);
 
 }  // namespace rkv

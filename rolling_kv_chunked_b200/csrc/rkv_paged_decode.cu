@@ -132,6 +132,11 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
   const int last_a = p.causal ? q.kv - q.n_q + ra / p.group : q.kv - 1;
   const int last_b = p.causal ? q.kv - q.n_q + rb / p.group : q.kv - 1;
   const int last_all = p.causal ? q.kv - q.n_q : q.kv - 1;
+  // where their scores go (a pair of places each), if they are kept
+  auto score_row = [&](int r) {
+    return (static_cast<long long>(q.q0 + r / p.group) * p.q_heads + h * p.group + r % p.group) * p.score_stride + cq;
+  };
+  const long long score_a = score_row(ra), score_b = score_row(rb);
   float o[16][4];
 #pragma unroll
   for (int i = 0; i < 16; ++i)
@@ -176,6 +181,15 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
 #pragma unroll
           for (int c = 0; c < 4; ++c)
             if (jw + i * 8 + cq + (c & 1) > (c < 2 ? last_a : last_b)) sc[i][c] = -INFINITY;
+      }
+      if (p.scores != nullptr) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (ra < rows)
+            *reinterpret_cast<float2*>(p.scores + score_a + jw + i * 8) = make_float2(sc[i][0], sc[i][1]);
+          if (rb < rows)
+            *reinterpret_cast<float2*>(p.scores + score_b + jw + i * 8) = make_float2(sc[i][2], sc[i][3]);
+        }
       }
       float xa = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));
       float xb = fmaxf(fmaxf(sc[0][2], sc[0][3]), fmaxf(sc[1][2], sc[1][3]));
@@ -367,7 +381,39 @@ __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const __
   }
 }
 
+// ---------------------------------------------------------------- attention weight of single tokens
+// The scores that the attention kept (masked ones -infinity) and the rows' log-sum-exp: a key gathers
+// the sum over the stream's at most 16 rows of 2^(score - z). One thread per key. Keeping a score costs 8
+// bytes of traffic per row and key; reading K again would cost 256 for all rows.
+constexpr int kTokenWeightThreads = 256;
+
+__global__ void __launch_bounds__(kTokenWeightThreads)
+    paged_token_weight_kernel(const __grid_constant__ PagedAttnParams p) {
+  const PagedView& w = p.view;
+  const int n_kt = (w.max_kv + kTokenWeightThreads - 1) / kTokenWeightThreads;
+  const int sh = blockIdx.x / n_kt;
+  const int h = sh % w.kv_heads, s = sh / w.kv_heads;
+  const int j = (blockIdx.x - sh * n_kt) * kTokenWeightThreads + threadIdx.x;
+  const PagedSeq q = paged_seq(w, s);
+  if (!q.ok || q.n_q == 0 || j >= q.kv) return;
+  float sum = 0.f;
+  for (int t = 0; t < q.n_q; ++t) {
+    const long long rh = static_cast<long long>(q.q0 + t) * p.q_heads + h * p.group;
+#pragma unroll 4
+    for (int g = 0; g < p.group; ++g)
+      sum += ptx::ex2(p.scores[(rh + g) * p.score_stride + j] - p.lse2[rh + g]);
+  }
+  float* to = p.weight + (static_cast<long long>(s) * w.kv_heads + h) * p.weight_stride + j;
+  *to = (j < q.kv - q.n_q ? *to : 0.f) + sum;
+}
+
 }  // namespace
+
+cudaError_t launch_paged_token_weight(const PagedAttnParams& p, cudaStream_t stream) {
+  const unsigned n_kt = (p.view.max_kv + kTokenWeightThreads - 1) / kTokenWeightThreads;
+  paged_token_weight_kernel<<<n_kt * p.view.n_seqs * p.view.kv_heads, kTokenWeightThreads, 0, stream>>>(p);
+  return cudaGetLastError();
+}
 
 cudaError_t launch_paged_decode(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const PagedAttnParams& p,
                                 cudaStream_t stream) {

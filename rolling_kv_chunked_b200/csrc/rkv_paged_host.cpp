@@ -37,7 +37,8 @@ int check_sizes(const rkv_page_pool* pool, const rkv_paged_batch* b, int n_rows)
   // a tensor map's stride and extents; the launch grids
   if (pool->page_stride >= (1LL << 38) || static_cast<long long>(pool->kv_heads) * p >= (1LL << 31) ||
       b->n_seqs > kMaxSeqs || static_cast<long long>(b->n_seqs) * pool->kv_heads >= (1LL << 24) ||
-      b->max_kv > (1 << 30))
+      b->max_kv > (1 << 30) ||
+      static_cast<long long>(b->n_seqs) * pool->kv_heads * ((b->max_kv + 127LL) / 128) >= (1LL << 30))
     return RKV_ERR_UNSUPPORTED;
   return RKV_OK;
 }
@@ -96,19 +97,31 @@ rkv::PagedPlan plan_of(const rkv_page_pool* pool, const rkv_paged_batch* b, int 
   std::memset(&p, 0, sizeof(p));
   const int group = q_heads / pool->kv_heads;
   p.rows_form = static_cast<long long>(b->max_q) * group <= rkv::kPagedRows;
-  p.block_tokens = b->max_q > 0 ? b->max_q : 1;
-  p.n_split = 1;
-  p.split_keys = b->max_kv > 0 ? b->max_kv : 1;
+  long long len = b->max_kv;
+  long long tile;
   if (p.rows_form) {
+    tile = rkv::kPagedDecodeTile;
+    p.block_tokens = b->max_q > 0 ? b->max_q : 1;
+    p.n_blocks = b->n_seqs;
     const long long blocks = static_cast<long long>(b->n_seqs) * pool->kv_heads;
     const long long want = 8LL * kSms;
-    long long len = (b->max_kv * blocks + want - 1) / want;
-    len = std::max<long long>(len, kMinSplit);
-    len = std::max<long long>(len, (b->max_kv + rkv::kPagedMaxSplit - 1) / rkv::kPagedMaxSplit);
-    len = (len + rkv::kPagedDecodeTile - 1) / rkv::kPagedDecodeTile * rkv::kPagedDecodeTile;
-    p.split_keys = static_cast<int>(len);
-    p.n_split = std::max(1, static_cast<int>((b->max_kv + len - 1) / len));
+    len = std::max<long long>((b->max_kv * blocks + want - 1) / want, kMinSplit);
+  } else {
+    tile = rkv::kKeyBox;
+    p.block_tokens = 2 * (rkv::kQueryBox / group);
+    const long long per_seq = (static_cast<long long>(b->max_q) + p.block_tokens - 1) / p.block_tokens;
+    p.n_blocks = static_cast<int>(std::min(static_cast<long long>(n_rows) / p.block_tokens + b->n_seqs,
+                                           static_cast<long long>(b->n_seqs) * per_seq));
+    const long long blocks = static_cast<long long>(p.n_blocks) * pool->kv_heads;
+    if (blocks > 0 && blocks < kSms) {
+      const long long want = (kSms + blocks - 1) / blocks;
+      len = std::max<long long>((b->max_kv + want - 1) / want, 2 * kMinSplit);
+    }
   }
+  len = std::max<long long>(len, (b->max_kv + rkv::kPagedMaxSplit - 1) / rkv::kPagedMaxSplit);
+  len = std::max<long long>((len + tile - 1) / tile * tile, tile);
+  p.split_keys = static_cast<int>(len);
+  p.n_split = std::max(1, static_cast<int>((b->max_kv + len - 1) / len));
   const long long heads = static_cast<long long>(n_rows) * q_heads;
   auto take = [&p](long long bytes) {
     const long long at = p.total;
@@ -118,6 +131,8 @@ rkv::PagedPlan plan_of(const rkv_page_pool* pool, const rkv_paged_batch* b, int 
   p.lse = weight ? take(4 * heads) : -1;
   p.part = p.n_split > 1 ? take(4 * heads * kHeadDim * p.n_split) : -1;
   p.part_ml = p.n_split > 1 ? take(8 * heads * p.n_split) : -1;
+  p.score_stride = (b->max_kv + 63LL) / 64 * 64;
+  p.scores = weight && p.rows_form ? take(4 * heads * p.score_stride) : -1;
   return p;
 }
 
@@ -202,23 +217,30 @@ RKV_API int rkv_paged_attention(const rkv_page_pool* pool, const rkv_paged_batch
   if (plan.lse >= 0) p.lse2 = reinterpret_cast<float*>(ws + plan.lse);
   if (plan.part >= 0) p.part = reinterpret_cast<float*>(ws + plan.part);
   if (plan.part_ml >= 0) p.part_ml = reinterpret_cast<float2*>(ws + plan.part_ml);
+  if (plan.scores >= 0) p.scores = reinterpret_cast<float*>(ws + plan.scores);
+  p.score_stride = plan.score_stride;
   p.block_tokens = plan.block_tokens;
+  p.n_blocks = plan.n_blocks;
   p.split_keys = plan.split_keys;
   p.n_split = plan.n_split;
   p.wait_limit_ns = kWaitNs;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t err;
+  CUtensorMap tm_q, tm_k, tm_v;
+  const int tile = plan.rows_form ? rkv::kPagedDecodeTile : rkv::kKeyBox;
+  if (!encode_pages(&tm_k, pool->k, pool, tile) || !encode_pages(&tm_v, pool->v, pool, tile)) return RKV_ERR_CUDA;
   if (plan.rows_form) {
-    CUtensorMap tm_k, tm_v;
-    if (!encode_pages(&tm_k, pool->k, pool, rkv::kPagedDecodeTile) ||
-        !encode_pages(&tm_v, pool->v, pool, rkv::kPagedDecodeTile))
-      return RKV_ERR_CUDA;
     err = rkv::launch_paged_decode(tm_k, tm_v, p, st);
+    if (err == cudaSuccess && plan.n_split > 1) err = rkv::launch_paged_combine(p, st);
+    if (err == cudaSuccess && weight != nullptr && batch->max_kv > 0) err = rkv::launch_paged_token_weight(p, st);
   } else {
-    err = rkv::launch_paged_attention(p, st);
+    if (!rkv::encode_map(&tm_q, q, q_heads, n_rows, kHeadDim * 2, static_cast<uint64_t>(q_stride) * 2, p.group,
+                         rkv::kQueryBox / p.group))
+      return RKV_ERR_CUDA;
+    err = rkv::launch_paged_chunk(tm_q, tm_k, tm_v, p, st);
+    if (err == cudaSuccess && plan.n_split > 1) err = rkv::launch_paged_combine(p, st);
+    if (err == cudaSuccess && weight != nullptr && batch->max_kv > 0) err = rkv::launch_paged_weight(tm_q, tm_k, p, st);
   }
-  if (err == cudaSuccess && plan.n_split > 1) err = rkv::launch_paged_combine(p, st);
-  if (err == cudaSuccess && weight != nullptr) err = rkv::launch_paged_weight(p, st);
   return cuda_rc(err);
 }
 
