@@ -227,6 +227,19 @@ __device__ __forceinline__ void tmem_st64(uint32_t taddr, const uint32_t (&r)[64
       : "memory");
 }
 
+// ------------------------------------------------------------------ asynchronous 16-byte copies
+__device__ __forceinline__ void cp_async16(uint32_t dst_smem, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst_smem), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+// Wait until at most kLeft of this thread's committed groups are in flight.
+template <int kLeft>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+
 // ------------------------------------------------------------------ warp matrix instructions
 // Four 8x8 matrices of 16-bit elements from shared memory: lane l gives the address of row l % 8 of
 // matrix l / 8, and receives elements 2 (l % 4), 2 (l % 4) + 1 of row l / 4 of each matrix.

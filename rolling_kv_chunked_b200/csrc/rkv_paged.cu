@@ -1,7 +1,10 @@
 // The paged cache's data movement: the write of a chunk into pages and eviction by weight.
-#include <algorithm>
+#include <cooperative_groups.h>
+
+#include <mutex>
 
 #include "paged.cuh"
+#include "ptx_sm100.cuh"
 
 namespace rkv {
 namespace {
@@ -44,170 +47,363 @@ __device__ __forceinline__ unsigned weight_key(float x) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+// A cluster of up to eight blocks chooses for one (stream, KV head). The weights are cut into equal runs,
+// one per warp of the cluster, in order; a lane holds its keys in registers (up to kHeldKeys; longer
+// streams are read from L2 again in every pass). The weight of rank `need` among the middle tokens is
+// found digit by digit (11, 11 and 10 bits of the ordered key: the first digit holds the exponent and
+// two bits of the fraction, so that equal digits, which collide in shared memory, are few): each block
+// counts its digits, after one cluster barrier every block adds up the histograms through
+// distributed shared memory and finds the digit for itself. Then each warp counts its kept tokens,
+// one more exchange gives every warp its place in the list, and the warps write their parts without
+// meeting again.
+// Measured, one stream of 65536 tokens and eight heads: 154 us with one block per head; in cycles of the
+// cluster form, per digit: counting 1000, the barrier 1650, the histograms 2100 (16 bytes a clock through
+// distributed shared memory: the held form therefore packs two counts to a word), finding 600.
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kSelCluster = 8;  // blocks of a cluster at most
+constexpr int kHeldKeys = 16;
 
-// Sum over the block's threads before this one (exclusive), and the block's total.
-__device__ __forceinline__ int block_scan(int x, int* warp_sums, int& total) {
-  const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
-  int inc = x;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, inc, d);
-    if (lane >= d) inc += y;
-  }
-  if (lane == 31) warp_sums[wp] = inc;
-  __syncthreads();
-  int before = 0, all = 0;
-  for (int i = 0; i < kSelWarps; ++i) {
-    if (i == wp) before = all;
-    all += warp_sums[i];
-  }
-  __syncthreads();
-  total = all;
-  return before + inc - x;
-}
-
-// One block per (stream, KV head). The weight of rank `need` among the middle tokens is found
-// digit by digit (11, 11 and 10 bits of the ordered key: the first digit holds the exponent
-// and two bits of the fraction, so that equal digits, which collide in shared memory, are
-// few); then one ordered pass lists the kept places and moves their weights.
+// kHeld: every warp's run has at most 32 * kHeldKeys tokens, a block's then less than 65536.
+template <bool kHeld>
 __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(const __grid_constant__ PagedEvictParams p) {
-  __shared__ int hist[2048];
+  namespace cg = cooperative_groups;
+  cg::cluster_group cluster = cg::this_cluster();
+  // counts of 2048 digits, by pass (a neighbour may still read the last pass's): two digits to a word if
+  // held, else one; thread t looks at the pair of digits 2t, 2t + 1
+  constexpr int kWords = kHeld ? 1 : 2;
+  struct __align__(4 * kWords) Pair {
+    unsigned x[kWords];
+  };
+  __shared__ Pair hist[3][kSelThreads];
   __shared__ int warp_sums[kSelWarps];
   __shared__ int found[2];
+  __shared__ int2 counts[kSelWarps];  // kept above the rank's weight (or fixed), and its equals, by warp
+  __shared__ int2 block_counts;
   const PagedView& w = p.view;
-  const int s = blockIdx.x / w.kv_heads;
+  const int size = static_cast<int>(cluster.num_blocks());
+  const int rank = blockIdx.x % size, sh = blockIdx.x / size;
+  const int s = sh / w.kv_heads;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n = __ldg(w.kv_len + s);
-  int* kept = p.kept + static_cast<long long>(blockIdx.x) * p.keep;
-  if (n < 0 || n > w.max_kv) {
-    if (threadIdx.x == 0) paged_report(w, kStatusLength);
-    for (int i = threadIdx.x; i < p.keep; i += kSelThreads) kept[i] = -1;
+  int* kept = p.kept + static_cast<long long>(sh) * p.keep;
+  const bool bad = n < 0 || n > w.max_kv;
+  if (bad || n <= p.keep) {  // the same in the whole cluster
+    if (bad && rank == 0 && threadIdx.x == 0) paged_report(w, kStatusLength);
+    for (int i = rank * kSelThreads + threadIdx.x; i < p.keep; i += size * kSelThreads)
+      kept[i] = !bad && i < n ? i : -1;
     return;
   }
-  if (n <= p.keep) {
-    for (int i = threadIdx.x; i < p.keep; i += kSelThreads) kept[i] = i < n ? i : -1;
-    return;
-  }
-  float* wt = p.weight + static_cast<long long>(blockIdx.x) * p.weight_stride;
+  const float* wt = p.weight + static_cast<long long>(sh) * p.weight_stride;
   const int a = p.sinks, b = n - p.recent;  // the middle: sinks + recent <= keep < n
   const int need = p.keep - p.sinks - p.recent;
+  // this warp's run of tokens
+  const int run = ((n + size * kSelWarps - 1) / (size * kSelWarps) + 31) / 32 * 32;
+  const int i0 = min(n, (rank * kSelWarps + warp) * run), i1 = min(n, i0 + run);
+
+  unsigned held[kHeldKeys];
+  if (kHeld) {
+#pragma unroll
+    for (int k = 0; k < kHeldKeys; ++k) {
+      const int i = i0 + 32 * k + lane;
+      held[k] = i < i1 ? weight_key(__ldg(wt + i)) : 0u;
+    }
+  }
+  // f(token, its key) for this lane's tokens, 32 tokens of the run at a time, in order
+  auto each = [&](auto f) {
+    if (kHeld) {
+#pragma unroll
+      for (int k = 0; k < kHeldKeys; ++k) {
+        if (i0 + 32 * k >= i1) break;
+        f(i0 + 32 * k + lane, held[k]);
+      }
+    } else {
+#pragma unroll 8
+      for (int i = i0; i < i1; i += 32) f(i + lane, i + lane < i1 ? weight_key(__ldg(wt + i + lane)) : 0u);
+    }
+  };
   unsigned prefix = 0, mask = 0;
   int rem = need;
-  for (int pass = 0; pass < 3 && need > 0; ++pass) {
-    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-    const int bins = pass == 2 ? 1024 : 2048;
-    for (int i = threadIdx.x; i < bins; i += kSelThreads) hist[i] = 0;
-    __syncthreads();
-    for (int i = a + threadIdx.x; i < b; i += kSelThreads) {
-      const unsigned u = weight_key(wt[i]);
-      if ((u & mask) == prefix) atomicAdd(&hist[(u >> shift) & (bins - 1)], 1);
+  for (int i = 0; i < 3; ++i)
+    for (int k = 0; k < kWords; ++k) hist[i][threadIdx.x].x[k] = 0u;
+  __syncthreads();
+  if (need > 0) {
+    for (int pass = 0; pass < 3; ++pass) {
+      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+      const unsigned top = pass == 2 ? 1023u : 2047u;
+      unsigned* mine = hist[pass][0].x;
+      each([&](int i, unsigned u) {
+        if (i < i1 && i >= a && i < b && (u & mask) == prefix) {
+          const unsigned digit = (u >> shift) & top;
+          if (kHeld)
+            atomicAdd(&mine[digit >> 1], (digit & 1) ? 0x10000u : 1u);
+          else
+            atomicAdd(&mine[digit], 1u);
+        }
+      });
+      cluster.sync();
+      // thread t owns two digits, from the top: 2 (1023 - t) and the one above
+      const int q = kSelThreads - 1 - static_cast<int>(threadIdx.x);
+      Pair part[kSelCluster];
+#pragma unroll
+      for (int r = 0; r < kSelCluster; ++r)  // all on their way at once; a smaller cluster reads some twice
+        part[r] = cluster.map_shared_rank(hist[pass], min(r, size - 1))[q];
+      int lo = 0, hi = 0;
+#pragma unroll
+      for (int r = 0; r < kSelCluster; ++r) {
+        const unsigned l = kHeld ? part[r].x[0] & 0xffffu : part[r].x[0];
+        const unsigned h = kHeld ? part[r].x[0] >> 16 : part[r].x[kWords - 1];
+        lo += r < size ? static_cast<int>(l) : 0;
+        hi += r < size ? static_cast<int>(h) : 0;
+      }
+      int inc = lo + hi;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, inc, d);
+        if (lane >= d) inc += y;
+      }
+      if (lane == 31) warp_sums[warp] = inc;
+      __syncthreads();
+      const int above = inc - lo - hi + __reduce_add_sync(0xffffffffu, lane < warp ? warp_sums[lane] : 0);
+      if (above < rem && rem <= above + hi) {
+        found[0] = 2 * q + 1;
+        found[1] = rem - above;
+      } else if (above + hi < rem && rem <= above + hi + lo) {
+        found[0] = 2 * q;
+        found[1] = rem - above - hi;
+      }
+      __syncthreads();
+      prefix |= static_cast<unsigned>(found[0]) << shift;
+      mask |= top << shift;
+      rem = found[1];
     }
-    __syncthreads();
-    // bins from the top: thread t owns the pair of bins bins - 2 - 2t, bins - 1 - 2t
-    const int hi = bins - 1 - 2 * static_cast<int>(threadIdx.x);
-    const int c1 = hi > 0 ? hist[hi] : 0, c0 = hi > 0 ? hist[hi - 1] : 0;
-    int total;
-    const int above = block_scan(c0 + c1, warp_sums, total);
-    if (above < rem && rem <= above + c1) {
-      found[0] = hi;
-      found[1] = rem - above;
-    } else if (above + c1 < rem && rem <= above + c1 + c0) {
-      found[0] = hi - 1;
-      found[1] = rem - above - c1;
-    }
-    __syncthreads();
-    prefix |= static_cast<unsigned>(found[0]) << shift;
-    mask |= static_cast<unsigned>(bins - 1) << shift;
-    rem = found[1];
-    __syncthreads();
   }
-  // ordered list: every key above the rank's, the first `rem` of its equals
-  int done = 0, ties = 0;
-  for (int base = 0; base < n; base += kSelThreads) {
-    const int i = base + threadIdx.x;
-    const float x = i < n ? wt[i] : 0.f;
-    const unsigned u = weight_key(x);
+  // every key above the rank's is kept, and the first `rem` of its equals
+  auto look = [&](int i, unsigned u, bool& take, bool& tie) {
     const bool mid = i >= a && i < b;
-    const bool tie = mid && need > 0 && u == prefix;
-    bool take = i < n && (!mid || (need > 0 && u > prefix));
-    int total;
-    const int rank = block_scan(tie ? 1 : 0, warp_sums, total);
-    if (tie && ties + rank < rem) take = true;
-    ties += total;
-    const int at = done + block_scan(take ? 1 : 0, warp_sums, total);
-    if (take) {
-      kept[at] = i;
-      wt[at] = x;  // at <= i, and this tile's weights were read before the barriers above
-    }
-    done += total;
+    take = i < i1 && (!mid || (need > 0 && u > prefix));
+    tie = i < i1 && mid && need > 0 && u == prefix;
+  };
+  int n_take = 0, n_tie = 0;
+  each([&](int i, unsigned u) {
+    bool take, tie;
+    look(i, u, take, tie);
+    n_take += take;
+    n_tie += tie;
+  });
+  n_take = __reduce_add_sync(0xffffffffu, n_take);
+  n_tie = __reduce_add_sync(0xffffffffu, n_tie);
+  if (lane == 0) counts[warp] = make_int2(n_take, n_tie);
+  __syncthreads();
+  const int2 mine = counts[lane];
+  int2 before;
+  before.x = __reduce_add_sync(0xffffffffu, lane < warp ? mine.x : 0);
+  before.y = __reduce_add_sync(0xffffffffu, lane < warp ? mine.y : 0);
+  if (warp == 0) {
+    const int all_x = __reduce_add_sync(0xffffffffu, mine.x), all_y = __reduce_add_sync(0xffffffffu, mine.y);
+    if (lane == 0) block_counts = make_int2(all_x, all_y);
   }
+  cluster.sync();
+  int2 neighbour = make_int2(0, 0);  // lane r: the counts of block r, if it comes before this one
+  if (lane < rank) neighbour = *cluster.map_shared_rank(&block_counts, lane);
+  cluster.barrier_arrive();  // no block leaves while a neighbour may read its counts
+  before.x += __reduce_add_sync(0xffffffffu, neighbour.x);
+  before.y += __reduce_add_sync(0xffffffffu, neighbour.y);
+  int ties = before.y;                       // equals of the rank's weight before this token
+  int at = before.x + min(before.y, rem);    // kept before this token
+  const unsigned below = (1u << lane) - 1u;
+  each([&](int i, unsigned u) {
+    bool take, tie;
+    look(i, u, take, tie);
+    const unsigned tied = __ballot_sync(0xffffffffu, tie);
+    if (tie && ties + __popc(tied & below) < rem) take = true;
+    ties += __popc(tied);
+    const unsigned taken = __ballot_sync(0xffffffffu, take);
+    if (take) kept[at + __popc(taken & below)] = i;
+    at += __popc(taken);
+  });
+  cluster.barrier_wait();
 }
 
 // ---------------------------------------------------------------- eviction: the move
-// Kept token i moves from place kept[i] >= i to place i, in order, within the same pages. A
-// block owns 16 / kMoveParts of the 16-byte columns of one (stream, KV head)'s K or V and walks
-// the list in tiles: a tile's sources are read before its places are written, and a later
-// tile's sources lie behind them.
+// Kept token i moves from place kept[i] >= i to place i, in order, within the same pages: a stable
+// compaction in place. The 256 bytes of a token are cut into two columns that never meet (128 bytes, a
+// line: columns of 32 bytes were bound by the lines that a warp's access touches), so
+// (stream, KV head, K or V, column) are independent blocks, each walking the list in tiles: a tile's
+// sources have been read by all before its places are written, and later tiles' sources lie behind
+// them, so two more tiles are on their way (cp.async into shared memory, each thread's 16 bytes its
+// own) while one is written. A cluster of blocks shares a tile's tokens where there are few heads. List entries and page ids are fetched ahead in registers: with a tile's
+// three dependent loads (entry, page id, data) in one row a tile took 3.6 us. One more block per
+// (stream, KV head) moves the weights.
 constexpr int kMoveThreads = 256;
-constexpr int kMoveParts = 8;
-constexpr int kMoveLanes = 16 / kMoveParts;            // lanes of one token
+constexpr int kMoveSteps = 4;   // 16-byte pieces of a tile per thread
+constexpr int kMoveAhead = 2;   // tiles in flight beside the one written
+constexpr int kMoveSmem = (kMoveAhead + 1) * kMoveSteps * kMoveThreads * 16;
+
+struct MoveList {
+  int first, count;
+};
+
+// Tokens kept, and the first that moves: kept[i] - i never decreases, -1 stands only at the end. The whole
+// block probes at once: two rounds for lists up to 262144, where a search by halves waits
+// for 2 log2(keep) loads in a row (10 us of the kernel's time at 16384).
+__device__ __forceinline__ MoveList move_list(const int* kept, int keep) {
+  int lo0 = 0, hi0 = keep, lo1 = 0, hi1 = keep;  // the count, the first that moves: in [lo, hi]
+  const int t = threadIdx.x;
+  while (lo0 < hi0 || lo1 < hi1) {
+    const int step0 = (hi0 - lo0 + kMoveThreads - 1) / kMoveThreads, step1 = (hi1 - lo1 + kMoveThreads - 1) / kMoveThreads;
+    const int i0 = lo0 + t * step0, i1 = lo1 + t * step1;
+    const bool there = step0 > 0 && i0 < hi0 && __ldg(kept + i0) >= 0;
+    const bool stays = step1 > 0 && i1 < hi1 && __ldg(kept + i1) == i1;
+    const int c0 = __syncthreads_count(there), c1 = __syncthreads_count(stays);
+    // c probes hold: the border lies behind the last of them, up to the next probe
+    hi0 = c0 == 0 ? lo0 : min(hi0, lo0 + c0 * step0);
+    lo0 = c0 == 0 ? lo0 : lo0 + (c0 - 1) * step0 + 1;
+    hi1 = c1 == 0 ? lo1 : min(hi1, lo1 + c1 * step1);
+    lo1 = c1 == 0 ? lo1 : lo1 + (c1 - 1) * step1 + 1;
+  }
+  MoveList r;
+  r.count = lo0;
+  r.first = min(lo1, lo0);
+  return r;
+}
+
+constexpr int kMoveParts = 2;                          // columns of a token
+constexpr int kMoveLanes = 16 / kMoveParts;             // lanes of one token, 16 bytes each
 constexpr int kMoveTokens = kMoveThreads / kMoveLanes;  // tokens per step
-constexpr int kMoveSteps = 8;
+constexpr int kMoveCluster = 8;                         // blocks of a cluster at most
 
 __global__ void __launch_bounds__(kMoveThreads) paged_move_kernel(const __grid_constant__ PagedEvictParams p) {
+  namespace cg = cooperative_groups;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int size = static_cast<int>(cluster.num_blocks()), rank = blockIdx.x % size;
   const PagedView& w = p.view;
-  int b = blockIdx.x;
-  const int part = b % kMoveParts;
-  b /= kMoveParts;
-  const bool is_v = b & 1;
-  b >>= 1;
+  const int heads = w.n_seqs * w.kv_heads;
+  const int task = blockIdx.x / size / heads, b = blockIdx.x / size % heads;
   const int h = b % w.kv_heads, s = b / w.kv_heads;
   const int* kept = p.kept + static_cast<long long>(b) * p.keep;
-  // tokens kept, and the first that moves: kept[i] - i never decreases, -1 only at the end
-  int lo = 0, hi = p.keep;
-  while (lo < hi) {
-    const int m = (lo + hi) >> 1;
-    if (kept[m] >= 0) lo = m + 1; else hi = m;
+  const MoveList m = move_list(kept, p.keep);
+  if (task == 2 * kMoveParts) {
+    if (rank != 0) return;
+    if (h == 0 && threadIdx.x == 0) p.kv_len_out[s] = m.count;
+    float* wt = p.weight + static_cast<long long>(b) * p.weight_stride;
+    for (int i0 = m.first; i0 < m.count; i0 += kMoveThreads * 8) {
+      float x[8];
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+        const int i = i0 + t * kMoveThreads + threadIdx.x;
+        if (i < m.count) x[t] = wt[__ldg(kept + i)];
+      }
+      __syncthreads();
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+        const int i = i0 + t * kMoveThreads + threadIdx.x;
+        if (i < m.count) wt[i] = x[t];
+      }
+      __syncthreads();
+    }
+    return;
   }
-  const int count = lo;
-  if (part == 0 && !is_v && h == 0 && threadIdx.x == 0) p.kv_len_out[s] = count;
-  lo = 0;
-  hi = count;
-  while (lo < hi) {
-    const int m = (lo + hi) >> 1;
-    if (kept[m] == m) lo = m + 1; else hi = m;
-  }
-  const int first = lo;
-  uint16_t* base = is_v ? w.v : w.k;
-  const int lane = threadIdx.x % kMoveLanes, tok = threadIdx.x / kMoveLanes;
-  const int c = (part * kMoveLanes + lane) * 8;
+  extern __shared__ uint4 pieces[];  // [tile][step][thread]
+  uint16_t* base = task >= kMoveParts ? w.v : w.k;
+  const int tok = threadIdx.x / kMoveLanes;
+  const int c = ((task % kMoveParts) * kMoveLanes + threadIdx.x % kMoveLanes) * 8;
   const int pm = (1 << w.page_shift) - 1;
-  for (int i0 = first; i0 < count; i0 += kMoveTokens * kMoveSteps) {
-    uint4 x[kMoveSteps];
-    bool have[kMoveSteps];
+  constexpr int kTileTokens = kMoveTokens * kMoveSteps;  // this block's share of a tile
+  const int n_tiles = (m.count - m.first + size * kTileTokens - 1) / (size * kTileTokens);
+  if (n_tiles == 0) return;
+  auto place = [&](int tile, int t) {
+    return m.first + (tile * size + rank) * kTileTokens + t * kMoveTokens + tok;
+  };
+  auto entry = [&](int tile, int t) {
+    const int i = place(tile, t);
+    return i < m.count ? __ldg(kept + i) : -1;
+  };
+  // the list's raw entry (-1 where there is no token): checked where it is used, a whole tile after
+  // its load was issued
+  const int* table = w.table + static_cast<long long>(s) * w.table_stride;
+  auto page = [&](int j) { return j >= 0 ? __ldg(table + (j >> w.page_shift)) : -1; };
+  auto checked = [&](int id, bool live) {
+    if (static_cast<unsigned>(id) < static_cast<unsigned>(w.n_pages)) return id;
+    if (live) paged_report(w, kStatusPage);
+    return -1;
+  };
+  // a tile is written where its source page and its own page are pages of the pool
+  unsigned good = 0;  // bit tile % 8 * 4 + step: fetched
+  auto mark = [&](int tile, int t, bool ok) {
+    const unsigned bit = 1u << ((tile & 7) * kMoveSteps + t);
+    good = ok ? good | bit : good & ~bit;
+  };
+  auto fetch = [&](int tile, int t, int raw, int from) {
+    const int id = checked(raw, from >= 0);
+    mark(tile, t, id >= 0);
+    if (id >= 0)
+      ptx::cp_async16(ptx::smem_u32(pieces + ((tile % (kMoveAhead + 1)) * kMoveSteps + t) * kMoveThreads + threadIdx.x),
+                      base + paged_offset(w, id, h, from & pm) + c);
+  };
+#pragma unroll
+  for (int tile = 0; tile < kMoveAhead; ++tile) {
 #pragma unroll
     for (int t = 0; t < kMoveSteps; ++t) {
-      const int i = i0 + t * kMoveTokens + tok;
-      have[t] = i < count;
-      if (have[t]) {
-        const int from = kept[i];
-        const int id = paged_id(w, s, from >> w.page_shift);
-        have[t] = id >= 0;
-        if (id >= 0) x[t] = *reinterpret_cast<const uint4*>(base + paged_offset(w, id, h, from & pm) + c);
-      }
+      const int from = entry(tile, t);
+      fetch(tile, t, page(from), from);
     }
-    __syncthreads();
-#pragma unroll
-    for (int t = 0; t < kMoveSteps; ++t) {
-      const int i = i0 + t * kMoveTokens + tok;
-      if (have[t]) {
-        const int id = paged_id(w, s, i >> w.page_shift);
-        if (id >= 0) *reinterpret_cast<uint4*>(base + paged_offset(w, id, h, i & pm) + c) = x[t];
-      }
-    }
-    __syncthreads();
+    ptx::cp_async_commit();
   }
+  int ahead[kMoveSteps], from[kMoveSteps], src[kMoveSteps], dst[kMoveSteps];
+#pragma unroll
+  for (int t = 0; t < kMoveSteps; ++t) {
+    from[t] = entry(kMoveAhead, t);
+    src[t] = page(from[t]);
+    ahead[t] = entry(kMoveAhead + 1, t);
+    dst[t] = page(place(0, t) < m.count ? place(0, t) : -1);
+  }
+  ptx::cp_async_wait<kMoveAhead - 1>();
+  cluster.barrier_arrive();  // this block has read its share of tile 0
+  for (int tile = 0; tile < n_tiles; ++tile) {
+    int to[kMoveSteps];
+#pragma unroll
+    for (int t = 0; t < kMoveSteps; ++t) {
+      fetch(tile + kMoveAhead, t, src[t], from[t]);
+      from[t] = ahead[t];
+      src[t] = page(from[t]);
+      ahead[t] = entry(tile + kMoveAhead + 2, t);
+      to[t] = dst[t];
+      const int i = place(tile + 1, t);
+      dst[t] = page(i < m.count ? i : -1);
+    }
+    ptx::cp_async_commit();
+    cluster.barrier_wait();  // the tile was read by all
+#pragma unroll
+    for (int t = 0; t < kMoveSteps; ++t) {
+      const bool got = good >> ((tile & 7) * kMoveSteps + t) & 1u;
+      const int id = checked(to[t], got);
+      if (got && id >= 0)
+        *reinterpret_cast<uint4*>(base + paged_offset(w, id, h, place(tile, t) & pm) + c) =
+            pieces[((tile % (kMoveAhead + 1)) * kMoveSteps + t) * kMoveThreads + threadIdx.x];
+    }
+    ptx::cp_async_wait<kMoveAhead - 1>();
+    cluster.barrier_arrive();  // the next one's share was read
+  }
+  cluster.barrier_wait();
+  ptx::cp_async_wait<0>();
+}
+
+// the dynamic shared-memory limit is a per-device setting, made once on every device this process
+// launches on
+cudaError_t configure() {
+  constexpr int kMaxDevices = 64;
+  static std::mutex mu;
+  static bool done[kMaxDevices] = {};
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lock(mu);
+  if (done[dev]) return cudaSuccess;
+  err = cudaFuncSetAttribute(paged_move_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMoveSmem);
+  if (err == cudaSuccess) done[dev] = true;
+  return err;
 }
 
 }  // namespace
@@ -220,11 +416,36 @@ cudaError_t launch_paged_write(const PagedWriteParams& p, cudaStream_t stream) {
 
 cudaError_t launch_paged_evict(const PagedEvictParams& p, cudaStream_t stream) {
   const unsigned heads = static_cast<unsigned>(p.view.n_seqs) * p.view.kv_heads;
-  paged_select_kernel<<<heads, kSelThreads, 0, stream>>>(p);
-  cudaError_t err = cudaGetLastError();
+  // blocks per cluster: as many as keep one block to an SM, each with at least 2048 tokens of the
+  // longest stream
+  constexpr unsigned kPlaces = 148;
+  unsigned size = kSelCluster;
+  while (size > 1 && (heads * size > kPlaces || static_cast<unsigned>(p.view.max_kv) < 2048u * size)) size /= 2;
+  const long long run = (p.view.max_kv + static_cast<long long>(size) * kSelWarps - 1) / (size * kSelWarps);
+  const bool held = run <= 32 * kHeldKeys;
+  cudaError_t err = configure();
   if (err != cudaSuccess) return err;
-  paged_move_kernel<<<heads * 2 * kMoveParts, kMoveThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = size;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(heads * size);
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  err = held ? cudaLaunchKernelEx(&cfg, paged_select_kernel<true>, p)
+             : cudaLaunchKernelEx(&cfg, paged_select_kernel<false>, p);
+  if (err != cudaSuccess) return err;
+  // blocks that share a column: up to eight, while the grid stays near three blocks to an SM
+  size = kMoveCluster;
+  while (size > 1 && heads * 2 * kMoveParts * size > 1024) size /= 2;
+  attr.val.clusterDim.x = size;
+  cfg.gridDim = dim3(heads * (2 * kMoveParts + 1) * size);
+  cfg.blockDim = dim3(kMoveThreads);
+  cfg.dynamicSmemBytes = kMoveSmem;
+  return cudaLaunchKernelEx(&cfg, paged_move_kernel, p);
 }
 
 }  // namespace rkv
