@@ -137,6 +137,8 @@ struct PagedView {
   int table_stride, n_seqs, n_rows, max_q, max_kv;
 };
 
+constexpr int kSmCount = 148;
+
 struct PagedWriteParams {
   PagedView view;
   const uint16_t* k;
@@ -148,15 +150,40 @@ struct PagedWriteParams {
 struct PagedPlan {
   int rows_form;     // 1: at most kPagedRows rows per stream and KV head, the form for single tokens
   int block_tokens;  // chunk tokens of one block of rows
-  int split_keys;    // cached tokens per part of a block's key stream
-  int n_split;       // parts at most
+  int split_keys;    // single-token form: cached tokens per part of a key stream
+  int n_split;       // and parts at most
   int n_blocks;      // blocks of chunk tokens in the batch at most
-  long long lse, part, part_ml, scores, total;  // -1: not used
+  long long lse, part, part_ml, scores, blocks, work, seq_first, total;  // -1: not used
   long long score_stride;
 };
 
 constexpr int kPagedRows = 16;
 constexpr int kPagedMaxSplit = 256;
+
+// Work of the chunk form, laid out on the device by a small kernel from the lengths of the moment
+// (workspace). A block of up to block_tokens chunk tokens of one stream, for every KV head the same:
+struct PagedBlock {
+  int row0, cnt;  // first row of the chunk tensors, tokens
+  int keys;       // cached tokens that its last row sees
+  int place0;     // the last place that its first row sees
+  int seq;
+  int start;      // key tiles of the blocks before it (one KV head)
+  int tiles;      // key tiles, at least 1
+  int unused;
+};
+// How the thread blocks share them. In a row: block c of n_ctas walks tiles [c W / n, (c + 1) W / n) of all
+// heads' tiles W. In step (units of nearly one size): every thread block takes `waves` whole units; of the
+// last n_tail, thread block i < n_tail takes the first `quota` tiles of unit i, and the others share
+// what is left of them, `quota` tiles each, in a row.
+struct PagedWork {
+  int n_blocks;
+  int head_tiles;  // key tiles of all blocks (one KV head)
+  int n_ctas;
+  int in_step;
+  int waves, n_tail, quota;
+  int rest[kSmCount + 1];  // in step: tiles left of the last units before unit i
+};
+constexpr int kPagedPartRows = 256;  // rows of a partial result of the chunk form
 
 struct PagedAttnParams {
   PagedView view;
@@ -169,8 +196,12 @@ struct PagedAttnParams {
   float scale_log2;  // log2(e) / sqrt(d)
   // workspace
   float* lse2;      // [n_rows][q_heads], log2; null when no weight is wanted
-  float* part;      // [n_split][n_rows][q_heads][128]: unnormalised sums of p v
-  float2* part_ml;  // [n_split][n_rows][q_heads]: reference (log2) and sum of p
+  float* part;      // single-token form: [n_split][n_rows][q_heads][128], unnormalised sums of p v;
+                    // chunk form: [2 * kSmCount][kPagedPartRows][128]
+  float2* part_ml;  // the same rows: reference (log2) and sum of p
+  PagedBlock* blocks;  // chunk form: [n_blocks]
+  PagedWork* work;
+  int* seq_first;      // chunk form: [n_seqs], the stream's first block
   float* scores;    // [n_rows][q_heads][score_stride]: log2 scores of the single-token form; null: not kept
   long long score_stride;
   int block_tokens, n_blocks, split_keys, n_split;

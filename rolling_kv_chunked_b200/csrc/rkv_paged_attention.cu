@@ -3,9 +3,18 @@
 //
 // Rows of one KV head's group of G query heads are packed into tiles of 128: row r of a tile is
 // token r / G, head r % G (128 / G whole tokens, loaded by one TMA box of G heads), so K and V are
-// read once for the group. A block takes 256 rows (two tiles) of one stream and KV head and walks the
-// pages; where a stream brings no more than 128 rows the two softmax warpgroups instead take
-// every second key tile of the one query tile and merge at the end.
+// read once for the group. A unit of work is 256 rows (two tiles) of one stream and KV head; where a
+// stream brings no more than 128 rows the two softmax warpgroups instead take every second key
+// tile of the one query tile and merge at the end.
+//
+// Lengths differ and are known on the device only, and 148 SMs take 264 equal units in two waves of which
+// the second is three quarters full. So one thread block per SM stays, and the blocks share the batch's
+// key tiles evenly: a small kernel (paged_plan_kernel) lists the units, counts their tiles and says how
+// they are shared (PagedWork), and units that are shared leave partial rows that paged_join_kernel adds up.
+// Lengths that differ are shared in a row, tile by tile. Units of nearly one size are shared in
+// step: then all blocks of a head read the same keys at the same time, from L2. (In a row, 24 heads of
+// 18480 tokens read their K and V from HBM eleven times over: 760 us, against 672 us for one thread
+// block per unit, although an eighth less of the machine idles.)
 //
 // Attention, structure of one block (as the rolling-window kernel's, rkv_attention.cu):
 //   warps 0-3, 4-7  softmax of query tile 0 / 1 (or of the even / odd key tiles)
@@ -32,8 +41,9 @@ constexpr int kThreads = 320;
 constexpr int kSmemQ = 0;
 constexpr int kSmemK = 2 * kTile;
 constexpr int kSmemV = 4 * kTile;
-constexpr int kSmemBar = 6 * kTile;
-constexpr int kSmemBytes = 6 * kTile + 256 + 1024;
+constexpr int kSmemChain = 6 * kTile;
+constexpr int kSmemBar = kSmemChain + 2 * 128 * 16;
+constexpr int kSmemBytes = kSmemBar + 256 + 1024;
 constexpr unsigned long long kDrainNs = 2000000000ull;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNoKey = -1e30f;        // reference (log2) of a row that has seen no key
@@ -51,8 +61,9 @@ enum : int {
   kBarPFull = 11,  // +softmax warpgroup
   kBarODone = 13,
   kBarDrain = 14,
-  kBarVFix = 15,   // the last tile's stale V rows were zeroed
-  kNumBars = 16
+  kBarVFix = 15,   // a unit's last tile's stale V rows were zeroed
+  kBarQEmpty = 16,  // every score product of a unit completed: its query buffer is free
+  kNumBars = 17
 };
 
 __device__ __forceinline__ constexpr uint32_t col_s(int t) { return static_cast<uint32_t>(t) * 128u; }
@@ -60,37 +71,237 @@ __device__ __forceinline__ constexpr uint32_t col_o(int t) { return 256u + stati
 constexpr uint32_t kIdescS = ptx::idesc_bf16_f32(kBM, kBN, false);
 constexpr uint32_t kIdescPV = ptx::idesc_bf16_f32(kBM, kHeadDim, true);
 
-// The block of chunk tokens that index b names, counted from the batch's last stream and its last
-// block down (under a causal mask a stream's last block sees most keys, so the long ones start
-// first). A whole warp calls it; returns false past the last block.
-__device__ __forceinline__ bool find_block(const PagedView& w, int b, int block_tokens, int& s, int& blk) {
-  const int lane = threadIdx.x & 31;
-  int before = 0;
-  for (int base = w.n_seqs - 1; base >= 0; base -= 32) {
-    const int i = base - lane;
-    int c = 0;
-    if (i >= 0) {
-      const PagedSeq q = paged_seq(w, i);
-      if (q.ok) c = (q.n_q + block_tokens - 1) / block_tokens;
-      else paged_report(w, kStatusLength);
-    }
-    int inc = c;
+// ---------------------------------------------------------------- the plan
+constexpr int kPlanThreads = 1024;
+constexpr int kMinTiles = 4;  // key tiles of a thread block's share at least
+
+// Exclusive sum over the thread block, and its total.
+__device__ __forceinline__ int plan_scan(int x, int* warp_sums, int& total) {
+  const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
+  int inc = x;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, inc, d);
-      if (lane >= d) inc += y;
+  for (int d = 1; d < 32; d <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, inc, d);
+    if (lane >= d) inc += y;
+  }
+  __syncthreads();
+  if (lane == 31) warp_sums[wp] = inc;
+  __syncthreads();
+  const int v = warp_sums[lane];
+  total = __reduce_add_sync(0xffffffffu, v);
+  return inc - x + __reduce_add_sync(0xffffffffu, lane < wp ? v : 0);
+}
+
+// One thread block: the units of the batch and their key tiles, from the lengths on the device.
+__global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_constant__ PagedAttnParams p) {
+  __shared__ int warp_sums[32];
+  const PagedView& w = p.view;
+  const int t = threadIdx.x;
+  int blocks = 0;
+  for (int base = 0; base < w.n_seqs; base += kPlanThreads) {
+    const int s = base + t;
+    int c = 0;
+    if (s < w.n_seqs) {
+      const PagedSeq q = paged_seq(w, s);
+      if (q.ok)
+        c = (q.n_q + p.block_tokens - 1) / p.block_tokens;
+      else
+        paged_report(w, kStatusLength);
     }
-    const unsigned hit = __ballot_sync(0xffffffffu, before + inc > b);
-    if (hit) {
-      const int l = __ffs(hit) - 1;
-      s = base - l;
-      blk = __shfl_sync(0xffffffffu, before + inc, l) - 1 - b;
+    int total;
+    const int first = blocks + plan_scan(c, warp_sums, total);
+    if (s < w.n_seqs) p.seq_first[s] = first;
+    blocks += total;
+  }
+  __syncthreads();
+  // row ranges that overlap (a start below an earlier one) can ask for more than the rows hold
+  if (blocks > p.n_blocks) {
+    if (t == 0) paged_report(w, kStatusLength);
+    blocks = p.n_blocks;
+  }
+  int tiles = 0, most = 0, least = 1 << 30;
+  for (int base = 0; base < blocks; base += kPlanThreads) {
+    const int b = base + t;
+    PagedBlock k = {};
+    if (b < blocks) {
+      int lo = 0, hi = w.n_seqs;  // the last stream whose first block is at or before b
+      while (hi - lo > 1) {
+        const int m = (lo + hi) >> 1;
+        if (p.seq_first[m] <= b) lo = m; else hi = m;
+      }
+      const PagedSeq q = paged_seq(w, lo);
+      const int i0 = (b - p.seq_first[lo]) * p.block_tokens;
+      k.row0 = q.q0 + i0;
+      k.cnt = min(p.block_tokens, q.n_q - i0);
+      k.keys = p.causal ? max(0, q.kv - q.n_q + i0 + k.cnt) : q.kv;
+      k.place0 = q.kv - q.n_q + i0;
+      k.seq = lo;
+      k.tiles = max(1, (k.keys + kBN - 1) / kBN);
+      most = max(most, k.tiles);
+      least = min(least, k.tiles);
+    }
+    int total;
+    k.start = tiles + plan_scan(k.tiles, warp_sums, total);
+    if (b < blocks) p.blocks[b] = k;
+    tiles += total;
+  }
+  // the whole block's largest and smallest
+  most = __reduce_max_sync(0xffffffffu, most);
+  least = __reduce_min_sync(0xffffffffu, least);
+  __syncthreads();
+  if ((t & 31) == 0) warp_sums[t >> 5] = most;
+  __syncthreads();
+  most = __reduce_max_sync(0xffffffffu, warp_sums[t & 31]);
+  __syncthreads();
+  if ((t & 31) == 0) warp_sums[t >> 5] = least;
+  __syncthreads();
+  least = __reduce_min_sync(0xffffffffu, warp_sums[t & 31]);
+
+  const long long units = static_cast<long long>(blocks) * w.kv_heads;
+  const long long all = static_cast<long long>(tiles) * w.kv_heads;
+  PagedWork* out = p.work;
+  const int waves = static_cast<int>(units / kSmCount), n_tail = static_cast<int>(units % kSmCount);
+  const long long first = static_cast<long long>(waves) * kSmCount;  // the first of the last units
+  int n = 0;  // thread i < n_tail: tiles of the i-th of them
+  if (t < n_tail) n = p.blocks[(first + t) % blocks].tiles;
+  int tail_tiles;
+  plan_scan(n, warp_sums, tail_tiles);
+  const int quota = (tail_tiles + kSmCount - 1) / kSmCount;
+  // in step: sizes within an eighth of each other, and shares worth a merge
+  const bool in_step = blocks > 0 && least >= most - most / 8 && (n_tail == 0 || quota >= kMinTiles);
+  int rest_tiles;
+  const int rest = plan_scan(max(0, n - quota), warp_sums, rest_tiles);
+  if (t <= n_tail) out->rest[t] = rest;
+  if (t == 0) {
+    out->n_blocks = blocks;
+    out->head_tiles = tiles;
+    out->in_step = in_step;
+    out->waves = waves;
+    out->n_tail = n_tail;
+    out->quota = quota;
+    out->n_ctas = in_step ? kSmCount
+                          : static_cast<int>(min(static_cast<long long>(kSmCount), (all + kMinTiles - 1) / kMinTiles));
+  }
+}
+
+// First tile of thread block c's share, counted over all heads.
+__device__ __forceinline__ long long share_start(const PagedWork& r, int kv_heads, int c) {
+  return static_cast<long long>(r.head_tiles) * kv_heads * c / r.n_ctas;
+}
+
+// The block of chunk tokens that holds tile y of a head. A whole warp calls it; 32 blocks are probed at
+// a time.
+__device__ __forceinline__ int find_block(const PagedBlock* blocks, int n, int y) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = n;  // the answer is the last block whose start is <= y: in [lo, hi)
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32;
+    const int i = lo + lane * step;
+    const bool le = i < hi && blocks[i].start <= y;
+    const int c = max(1, __popc(__ballot_sync(0xffffffffu, le)));
+    hi = min(hi, lo + c * step);
+    lo += (c - 1) * step;
+  }
+  return lo;
+}
+
+// In step: the thread block (of those past n_tail, counted from 0) that takes leftover tile y.
+__device__ __forceinline__ int helper_of(const PagedWork& r, int y) {
+  return min(kSmCount - r.n_tail - 1, y / r.quota);
+}
+
+// A unit, or the part of one, that a thread block works on.
+struct PagedUnit {
+  PagedBlock k;
+  int h;
+  int t0, t1;  // its key tiles
+  int slot;    // of a part: where its rows go
+  bool two;    // two query tiles
+  int j0, n_tiles, last_valid;  // first key, tiles, visible keys of the last tile
+};
+
+// The units of one thread block's share, in order; every role of the block walks them by itself.
+struct PagedWalk {
+  const PagedBlock* blocks;
+  const PagedWork* work;
+  int n_blocks, tpt, cta;
+  bool in_step;
+  int wave;        // in step: whole units taken
+  long long left;  // tiles of the share still to take (in step: of the last units)
+  int h, b, t;     // the next unit's head, block and first tile
+  int i, pos;      // in step, of a helper: the last unit it is at, and the next leftover tile
+
+  __device__ __forceinline__ void take(PagedUnit& u, long long most) {
+    const int4* src = reinterpret_cast<const int4*>(blocks + b);
+    const int4 x = src[0], y = src[1];
+    u.k.row0 = x.x;
+    u.k.cnt = x.y;
+    u.k.keys = x.z;
+    u.k.place0 = x.w;
+    u.k.seq = y.x;
+    u.k.start = y.y;
+    u.k.tiles = y.z;
+    u.h = h;
+    u.t0 = t;
+    u.t1 = static_cast<int>(min(static_cast<long long>(u.k.tiles), t + most));
+    u.two = u.k.cnt > tpt;
+    u.j0 = t * kBN;
+    u.n_tiles = u.t1 - t;
+    u.last_valid = min(kBN, u.k.keys - (u.t1 - 1) * kBN);
+  }
+  __device__ __forceinline__ void at_unit(long long n) {
+    h = static_cast<int>(n / n_blocks);
+    b = static_cast<int>(n - static_cast<long long>(h) * n_blocks);
+  }
+  __device__ __forceinline__ bool next(PagedUnit& u) {
+    if (!in_step) {
+      if (left <= 0) return false;
+      take(u, left);
+      // this thread block's first slot if the unit began before its share, else its second
+      u.slot = 2 * cta + (t == 0 ? 1 : 0);
+      left -= u.n_tiles;
+      t = 0;
+      if (++b == n_blocks) {
+        b = 0;
+        ++h;
+      }
       return true;
     }
-    before += __shfl_sync(0xffffffffu, inc, 31);
+    t = 0;
+    if (wave < work->waves) {
+      at_unit(cta + static_cast<long long>(wave) * kSmCount);
+      take(u, 1 << 30);
+      ++wave;
+      return true;
+    }
+    const long long first = static_cast<long long>(work->waves) * kSmCount;
+    const int n_tail = work->n_tail;
+    if (cta < n_tail) {
+      if (left <= 0) return false;
+      left = 0;
+      at_unit(first + cta);
+      take(u, work->quota);
+      u.slot = 2 * cta + helper_of(*work, work->rest[cta]);
+      return true;
+    }
+    // a helper: leftover tiles [pos, pos + left) in a row
+    while (left > 0) {
+      const int begin = work->rest[i], end = work->rest[i + 1];
+      if (pos >= end) {
+        ++i;
+        continue;
+      }
+      at_unit(first + i);
+      t = work->quota + pos - begin;
+      take(u, left);
+      u.slot = 2 * i + cta - n_tail + 1;
+      pos += u.n_tiles;
+      left -= u.n_tiles;
+      return true;
+    }
+    return false;
   }
-  return false;
-}
+};
 
 // 2^x on the FMA pipe for two lanes: r = round(x) by adding 1.5 * 2^23, f = x - r in [-1/2, 1/2], a
 // polynomial for 2^f fitted for least relative error (tests/exp2_poly.py; degree 4: 2.7e-6, mean
@@ -252,6 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PagedAttnParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float4* chain = reinterpret_cast<float4*>(smem + kSmemChain);  // [2][128]: reference, sum, pending factor
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kSmemBar);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kNumBars);
   int* found = reinterpret_cast<int*>(bars + kNumBars + 1);
@@ -259,18 +471,48 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const unsigned long long limit = p.wait_limit_ns;
 
-  const int sp = blockIdx.x % p.n_split;
-  const int u = blockIdx.x / p.n_split;
-  const int h = u / p.n_blocks;
+  const PagedWork& work = *p.work;
+  const int cta = blockIdx.x;
+  if (cta >= work.n_ctas) return;
+  const int G = p.group;
+  const int tpt = kBM / G;  // tokens of a query tile
+  PagedWalk walk;
+  walk.blocks = p.blocks;
+  walk.work = &work;
+  walk.n_blocks = work.n_blocks;
+  walk.tpt = tpt;
+  walk.cta = cta;
+  walk.in_step = work.in_step != 0;
+  walk.wave = walk.i = walk.pos = 0;
+  int y0 = 0;
+  if (!walk.in_step) {
+    const long long x0 = share_start(work, w.kv_heads, cta);
+    walk.left = share_start(work, w.kv_heads, cta + 1) - x0;
+    walk.h = static_cast<int>(x0 / work.head_tiles);
+    y0 = static_cast<int>(x0 - static_cast<long long>(walk.h) * work.head_tiles);
+  } else if (cta < work.n_tail) {
+    walk.left = work.quota;
+  } else {
+    const int all = work.rest[work.n_tail];
+    walk.pos = min(all, (cta - work.n_tail) * work.quota);
+    walk.left = (cta == kSmCount - 1 ? all : min(all, walk.pos + work.quota)) - walk.pos;
+    int hi = work.n_tail;  // the last unit whose leftover begins at or before pos
+    while (hi - walk.i > 1) {
+      const int m = (walk.i + hi) >> 1;
+      if (work.rest[m] <= walk.pos) walk.i = m; else hi = m;
+    }
+  }
   if (warp == 0) {
-    int s = -1, blk = 0;
-    if (!find_block(w, u - h * p.n_blocks, p.block_tokens, s, blk)) s = -1;
-    if (lane == 0) {
-      found[0] = s;
-      found[1] = blk;
+    if (!walk.in_step) {
+      const int b = find_block(p.blocks, work.n_blocks, y0);
+      if (lane == 0) {
+        found[0] = b;
+        found[1] = p.blocks[b].start;
+      }
     }
   } else if (threadIdx.x == 32) {
     ptx::mbar_init(&bars[kBarQ], 1);
+    ptx::mbar_init(&bars[kBarQEmpty], 1);
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&bars[kBarKFull + i], 1);
       ptx::mbar_init(&bars[kBarKEmpty + i], 1);
@@ -283,24 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::mbar_init(&bars[kBarDrain], 1);
     ptx::mbar_init(&bars[kBarVFix], 1);
     ptx::fence_mbar_init();
-  }
-  __syncthreads();
-  const int s = found[0], blk = found[1];
-  if (s < 0) return;
-  const PagedSeq q = paged_seq(w, s);
-  const int G = p.group;
-  const int tpt = kBM / G;                 // tokens of a query tile
-  const int i0 = blk * p.block_tokens;     // the block's first chunk token
-  const int cnt = min(p.block_tokens, q.n_q - i0);
-  const bool two = cnt > tpt;
-  const int keys = p.causal ? max(0, q.kv - q.n_q + i0 + cnt) : q.kv;  // seen by the block's last row
-  const int j0 = sp * p.split_keys;
-  if (j0 >= keys && (sp > 0 || p.n_split > 1)) return;
-  const int j1 = min(keys, j0 + p.split_keys);
-  const int n_tiles = (j1 - j0 + kBN - 1) / kBN;  // 0 only when the rows see nothing at all
-  const int last_valid = j1 - j0 - (n_tiles - 1) * kBN;
-
-  if (warp == 9) {
+  } else if (warp == 9) {
     ptx::tmem_alloc(tmem_slot, 512);
     ptx::tmem_relinquish();
   }
@@ -315,141 +540,174 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  if (!walk.in_step) {
+    walk.b = found[0];
+    walk.t = y0 - found[1];
+  }
+  PagedUnit u;
 
   if (warp == 8) {
     // ------------------------------------------------------------ TMA producer
+    const int box = min(1 << w.page_shift, kBN);  // tokens per copy
+    const int n_box = kBN / box;
+    const int b = lane % n_box, c = (lane / n_box) & 1;
+    const bool is_v = (lane / n_box) & 2, mine = lane < 4 * n_box;
+    const CUtensorMap* tm = is_v ? &tm_v : &tm_k;
+    uint8_t* dst = smem + (is_v ? kSmemV : kSmemK) + c * kSlab + b * box * 128;
+    if (lane == 0) {
+      ptx::prefetch_tmap(&tm_q);
+      ptx::prefetch_tmap(&tm_k);
+      ptx::prefetch_tmap(&tm_v);
+    }
     bool ok = true;
-    int nk = 0, nv = 0;
-    if (n_tiles > 0) {
-      const int box = min(1 << w.page_shift, kBN);  // tokens per copy
-      const int n_box = kBN / box;
-      const int b = lane % n_box, c = (lane / n_box) & 1;
-      const bool is_v = (lane / n_box) & 2, mine = lane < 4 * n_box;
-      const CUtensorMap* tm = is_v ? &tm_v : &tm_k;
-      uint8_t* dst = smem + (is_v ? kSmemV : kSmemK) + c * kSlab + b * box * 128;
-      if (lane == 0) {
-        ptx::prefetch_tmap(&tm_k);
-        ptx::prefetch_tmap(&tm_v);
-        ptx::mbar_arrive_expect_tx(&bars[kBarQ], (two ? 2 : 1) * 2 * 128 * tpt * G);
-        for (int t = 0; t < (two ? 2 : 1); ++t)
-          for (int cc = 0; cc < 2; ++cc)
-            ptx::tma_load_3d(smem + kSmemQ + t * kTile + cc * kSlab, &tm_q, &bars[kBarQ], cc * 64, h * G,
-                             q.q0 + i0 + t * tpt);
+    int nq = 0, nk = 0, nv = 0;  // units' queries, K and V tiles issued
+    while (ok && walk.next(u)) {
+      if (nq > 0) {
+        ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars[kBarQEmpty], (nq - 1) & 1, limit));
+        if (!ok) break;
       }
+      if (lane == 0) {
+        ptx::mbar_arrive_expect_tx(&bars[kBarQ], (u.two ? 2 : 1) * 2 * 128 * tpt * G);
+        for (int t = 0; t < (u.two ? 2 : 1); ++t)
+          for (int cc = 0; cc < 2; ++cc)
+            ptx::tma_load_3d(smem + kSmemQ + t * kTile + cc * kSlab, &tm_q, &bars[kBarQ], cc * 64, u.h * G,
+                             u.k.row0 + t * tpt);
+      }
+      ++nq;
+      const int j1 = min(u.k.keys, u.t1 * kBN);
       int id = -1;
-      if (mine && j0 + b * box < j1) id = paged_id(w, s, (j0 + b * box) >> w.page_shift);
-      for (int t = 0; t < n_tiles; ++t) {
-        const int st = t & 1;
-        const int j = j0 + t * kBN + b * box;
+      if (mine && u.j0 + b * box < j1) id = paged_id(w, u.k.seq, (u.j0 + b * box) >> w.page_shift);
+      for (int t = 0; t < u.n_tiles; ++t) {
+        const int st = nk & 1;
+        const int j = u.j0 + t * kBN + b * box;
         const int page = max(id, 0);
-        if (mine && j + kBN < j1) id = paged_id(w, s, (j + kBN) >> w.page_shift);
-        const int bytes = (min(kBN, j1 - j0 - t * kBN) + box - 1) / box * box * 256;
-        const int row = (h << w.page_shift) + (j & ((1 << w.page_shift) - 1));
-        if (t >= 2) {
-          ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars[kBarKEmpty + st], ((t - 2) >> 1) & 1, limit));
+        if (mine && j + kBN < j1) id = paged_id(w, u.k.seq, (j + kBN) >> w.page_shift);
+        const int bytes = (max(0, min(kBN, j1 - u.j0 - t * kBN)) + box - 1) / box * box * 256;
+        const int row = (u.h << w.page_shift) + (j & ((1 << w.page_shift) - 1));
+        if (nk >= 2) {
+          ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars[kBarKEmpty + st], ((nk - 2) >> 1) & 1, limit));
           if (!ok) break;
         }
         if (lane == 0) ptx::mbar_arrive_expect_tx(&bars[kBarKFull + st], bytes);
         __syncwarp();
         if (mine && !is_v && j < j1) ptx::tma_load_3d(dst + st * kTile, tm, &bars[kBarKFull + st], c * 64, row, page);
-        nk = t + 1;
-        if (t >= 2) {
-          ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars[kBarVEmpty + st], ((t - 2) >> 1) & 1, limit));
+        ++nk;
+        if (nv >= 2) {
+          ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars[kBarVEmpty + st], ((nv - 2) >> 1) & 1, limit));
           if (!ok) break;
         }
         if (lane == 0) ptx::mbar_arrive_expect_tx(&bars[kBarVFull + st], bytes);
         __syncwarp();
         if (mine && is_v && j < j1) ptx::tma_load_3d(dst + st * kTile, tm, &bars[kBarVFull + st], c * 64, row, page);
-        nv = t + 1;
+        ++nv;
       }
       // the last tile's V rows from the last visible token to the end of its step of 16
-      if (ok && (last_valid & 15)) {
-        const int t = n_tiles - 1;
-        ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars[kBarVFull + (t & 1)], (t >> 1) & 1, limit));
+      if (ok && (u.last_valid & 15)) {
+        const int st = (nv - 1) & 1;
+        ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars[kBarVFull + st], ((nv - 1) >> 1) & 1, limit));
         if (ok) {
-          const int end = (last_valid + 15) & ~15;
-          for (int i = lane; i < (end - last_valid) * 16; i += 32)
-            *reinterpret_cast<uint4*>(smem + kSmemV + (t & 1) * kTile + ((i >> 3) & 1) * kSlab +
-                                      (last_valid + (i >> 4)) * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
+          const int end = (u.last_valid + 15) & ~15;
+          for (int i = lane; i < (end - u.last_valid) * 16; i += 32)
+            *reinterpret_cast<uint4*>(smem + kSmemV + st * kTile + ((i >> 3) & 1) * kSlab +
+                                      (u.last_valid + (i >> 4)) * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
           ptx::fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(&bars[kBarVFix]);
         }
       }
-      if (lane == 0) {
-        if (!ok) paged_report(w, kStatusTimeout);
-        // every copy issued must land before the block may exit
-        ptx::mbar_wait(&bars[kBarQ], 0, kDrainNs);
-        for (int t = max(0, nk - 2); t < nk; ++t) ptx::mbar_wait(&bars[kBarKFull + (t & 1)], (t >> 1) & 1, kDrainNs);
-        for (int t = max(0, nv - 2); t < nv; ++t) ptx::mbar_wait(&bars[kBarVFull + (t & 1)], (t >> 1) & 1, kDrainNs);
-      }
+    }
+    if (lane == 0) {
+      if (!ok) paged_report(w, kStatusTimeout);
+      // every copy issued must land before the thread block may exit
+      if (nq > 0) ptx::mbar_wait(&bars[kBarQ], (nq - 1) & 1, kDrainNs);
+      for (int t = max(0, nk - 2); t < nk; ++t) ptx::mbar_wait(&bars[kBarKFull + (t & 1)], (t >> 1) & 1, kDrainNs);
+      for (int t = max(0, nv - 2); t < nv; ++t) ptx::mbar_wait(&bars[kBarVFull + (t & 1)], (t >> 1) & 1, kDrainNs);
     }
     __syncwarp();
   } else if (warp == 9) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0 && n_tiles > 0) {
-      const uint32_t q_addr[2] = {ptx::smem_u32(smem + kSmemQ), ptx::smem_u32(smem + kSmemQ + (two ? kTile : 0))};
+    if (lane == 0) {
       const uint32_t k_addr = ptx::smem_u32(smem + kSmemK);
       const uint32_t v_addr = ptx::smem_u32(smem + kSmemV);
-      bool ok = ptx::mbar_wait(&bars[kBarQ], 0, limit);
-      auto issue_s = [&](int t, uint32_t kt) {
+      bool ok = true;
+      int g0 = 0;                 // tiles of the units before this one
+      int used[2] = {0, 0};       // P tiles that each accumulator took before this unit
+      int n_unit = 0, n_fix = 0;  // units, and those whose last V tile was mended
+      while (ok && walk.next(u)) {
+        const uint32_t q_addr[2] = {ptx::smem_u32(smem + kSmemQ), ptx::smem_u32(smem + kSmemQ + (u.two ? kTile : 0))};
+        const bool fix = (u.last_valid & 15) != 0;
+        auto issue_s = [&](int t, uint32_t kt) {
 #pragma unroll
-        for (int kk = 0; kk < kHeadDim / 16; ++kk)
-          ptx::mma_ss(tmem + col_s(t), desc_kmajor(q_addr[t], kk), desc_kmajor(kt, kk), kIdescS, kk > 0 ? 1u : 0u);
-      };
-      // V of tile j observed, the last one's stale rows zeroed
-      auto wait_v = [&](int j) -> bool {
-        if (!ptx::mbar_wait(&bars[kBarVFull + (j & 1)], (j >> 1) & 1, limit)) return false;
-        return j + 1 < n_tiles || (last_valid & 15) == 0 || ptx::mbar_wait(&bars[kBarVFix], 0, limit);
-      };
-      // O_t += P_t V(j), the use-th of its accumulator; V(j) already observed
-      auto issue_pv = [&](int t, int j, int use, bool frees_v) -> bool {
-        if (!ptx::mbar_wait(&bars[kBarPFull + t], use & 1, limit)) return false;
-        ptx::tc_fence_after();
-        const uint32_t vt = v_addr + (j & 1) * kTile;
-        const int steps = j + 1 < n_tiles ? kBN / 16 : (last_valid + 15) >> 4;
+          for (int kk = 0; kk < kHeadDim / 16; ++kk)
+            ptx::mma_ss(tmem + col_s(t), desc_kmajor(q_addr[t], kk), desc_kmajor(kt, kk), kIdescS, kk > 0 ? 1u : 0u);
+        };
+        auto wait_k = [&](int j) {
+          return ptx::mbar_wait(&bars[kBarKFull + ((g0 + j) & 1)], ((g0 + j) >> 1) & 1, limit);
+        };
+        // V of tile j observed, the unit's last one's stale rows zeroed
+        auto wait_v = [&](int j) -> bool {
+          if (!ptx::mbar_wait(&bars[kBarVFull + ((g0 + j) & 1)], ((g0 + j) >> 1) & 1, limit)) return false;
+          return j + 1 < u.n_tiles || !fix || ptx::mbar_wait(&bars[kBarVFix], n_fix & 1, limit);
+        };
+        // O_t += P_t V(j), the use-th of the unit into this accumulator; V(j) already observed
+        auto issue_pv = [&](int t, int j, int use, bool frees_v) -> bool {
+          if (!ptx::mbar_wait(&bars[kBarPFull + t], (used[t] + use) & 1, limit)) return false;
+          ptx::tc_fence_after();
+          const uint32_t vt = v_addr + ((g0 + j) & 1) * kTile;
+          const int steps = j + 1 < u.n_tiles ? kBN / 16 : (u.last_valid + 15) >> 4;
 #pragma unroll
-        for (int kk = 0; kk < kBN / 16; ++kk)
-          if (kk < steps)
-            ptx::mma_ts(tmem + col_o(t), tmem + col_s(t) + kk * 8, desc_v(vt, kk), kIdescPV,
-                        (use > 0 || kk > 0) ? 1u : 0u);
-        if (frees_v) ptx::mma_commit(&bars[kBarVEmpty + (j & 1)]);
-        return true;
-      };
-      if (two) {
-        // S0(j), PV1(j-1), S1(j), PV0(j): one warpgroup's softmax beside the other tile's products;
-        // the waits on V(j) and K(j+1) are taken before the wait for P0(j), where this thread idles
-        bool k_ready = ok && ptx::mbar_wait(&bars[kBarKFull], 0, limit);
-        if (!k_ready) ok = false;
-        for (int j = 0; ok && j < n_tiles; ++j) {
-          const int st = j & 1;
-          if (!k_ready && !ptx::mbar_wait(&bars[kBarKFull + st], (j >> 1) & 1, limit)) { ok = false; break; }
-          ptx::tc_fence_after();
-          const uint32_t kt = k_addr + st * kTile;
-          issue_s(0, kt);
-          ptx::mma_commit(&bars[kBarSFull + 0]);
-          if (j > 0 && !issue_pv(1, j - 1, j - 1, true)) { ok = false; break; }
-          issue_s(1, kt);
-          ptx::mma_commit(&bars[kBarSFull + 1]);
-          ptx::mma_commit(&bars[kBarKEmpty + st]);
-          if (!wait_v(j)) { ok = false; break; }
-          k_ready = j + 1 < n_tiles && ptx::mbar_try_wait(&bars[kBarKFull + (st ^ 1)], ((j + 1) >> 1) & 1);
-          if (!issue_pv(0, j, j, false)) { ok = false; break; }
+          for (int kk = 0; kk < kBN / 16; ++kk)
+            if (kk < steps)
+              ptx::mma_ts(tmem + col_o(t), tmem + col_s(t) + kk * 8, desc_v(vt, kk), kIdescPV,
+                          (use > 0 || kk > 0) ? 1u : 0u);
+          if (frees_v) ptx::mma_commit(&bars[kBarVEmpty + ((g0 + j) & 1)]);
+          return true;
+        };
+        if (!ptx::mbar_wait(&bars[kBarQ], n_unit & 1, limit)) { ok = false; break; }
+        if (u.two) {
+          // S0(j), PV1(j-1), S1(j), PV0(j): one warpgroup's softmax beside the other tile's products;
+          // the waits on V(j) and K(j+1) are taken before the wait for P0(j), where this thread idles
+          bool k_ready = wait_k(0);
+          if (!k_ready) ok = false;
+          for (int j = 0; ok && j < u.n_tiles; ++j) {
+            if (!k_ready && !wait_k(j)) { ok = false; break; }
+            ptx::tc_fence_after();
+            const uint32_t kt = k_addr + ((g0 + j) & 1) * kTile;
+            issue_s(0, kt);
+            ptx::mma_commit(&bars[kBarSFull + 0]);
+            if (j > 0 && !issue_pv(1, j - 1, j - 1, true)) { ok = false; break; }
+            issue_s(1, kt);
+            ptx::mma_commit(&bars[kBarSFull + 1]);
+            ptx::mma_commit(&bars[kBarKEmpty + ((g0 + j) & 1)]);
+            if (j + 1 == u.n_tiles) ptx::mma_commit(&bars[kBarQEmpty]);
+            if (!wait_v(j)) { ok = false; break; }
+            k_ready = j + 1 < u.n_tiles && ptx::mbar_try_wait(&bars[kBarKFull + ((g0 + j + 1) & 1)], ((g0 + j + 1) >> 1) & 1);
+            if (!issue_pv(0, j, j, false)) { ok = false; break; }
+          }
+          if (ok && !issue_pv(1, u.n_tiles - 1, u.n_tiles - 1, true)) ok = false;
+          used[0] += u.n_tiles;
+          used[1] += u.n_tiles;
+        } else {
+          // two chains over the one query tile: S(j) into buffer j & 1 while the other's softmax runs
+          for (int j = 0; ok && j < u.n_tiles; ++j) {
+            if (!wait_k(j)) { ok = false; break; }
+            ptx::tc_fence_after();
+            issue_s(j & 1, k_addr + ((g0 + j) & 1) * kTile);
+            ptx::mma_commit(&bars[kBarSFull + (j & 1)]);
+            ptx::mma_commit(&bars[kBarKEmpty + ((g0 + j) & 1)]);
+            if (j + 1 == u.n_tiles) ptx::mma_commit(&bars[kBarQEmpty]);
+            if (j > 0 && !(wait_v(j - 1) && issue_pv((j - 1) & 1, j - 1, (j - 1) >> 1, true))) ok = false;
+          }
+          const int j = u.n_tiles - 1;
+          if (ok && !(wait_v(j) && issue_pv(j & 1, j, j >> 1, true))) ok = false;
+          used[0] += (u.n_tiles + 1) >> 1;
+          used[1] += u.n_tiles >> 1;
         }
-        if (ok && !issue_pv(1, n_tiles - 1, n_tiles - 1, true)) ok = false;
-      } else {
-        // two chains over the one query tile: S(j) into buffer j & 1 while the other's softmax runs
-        for (int j = 0; ok && j < n_tiles; ++j) {
-          if (!ptx::mbar_wait(&bars[kBarKFull + (j & 1)], (j >> 1) & 1, limit)) { ok = false; break; }
-          ptx::tc_fence_after();
-          issue_s(j & 1, k_addr + (j & 1) * kTile);
-          ptx::mma_commit(&bars[kBarSFull + (j & 1)]);
-          ptx::mma_commit(&bars[kBarKEmpty + (j & 1)]);
-          if (j > 0 && !(wait_v(j - 1) && issue_pv((j - 1) & 1, j - 1, (j - 1) >> 1, true))) ok = false;
-        }
-        if (ok && !(wait_v(n_tiles - 1) && issue_pv((n_tiles - 1) & 1, n_tiles - 1, (n_tiles - 1) >> 1, true))) ok = false;
+        if (ok) ptx::mma_commit(&bars[kBarODone]);
+        g0 += u.n_tiles;
+        n_fix += fix;
+        ++n_unit;
       }
-      if (ok) ptx::mma_commit(&bars[kBarODone]);
       if (!ok) paged_report(w, kStatusTimeout);
       // everything issued must complete before TMEM is released
       ptx::mma_commit(&bars[kBarDrain]);
@@ -464,110 +722,178 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tS = lane_base + col_s(wg), tO = lane_base + col_o(wg);
     const float sl2 = p.scale_log2;
     const uint64_t c2 = ptx::f2_pack(sl2, sl2);
-    const int tile0 = two ? wg * tpt : 0;  // this query tile's first token in the block
     const int tok = r / G;
-    const bool live = r < min(tpt, cnt - tile0) * G;
-    // the last place this row sees; rows of no token see what the block sees, so that they
-    // hold no whole warp on the masked path
-    const int last = p.causal && live ? q.kv - q.n_q + i0 + tile0 + tok : keys - 1;
-    const int n_mine = two ? n_tiles : (n_tiles + 1 - wg) >> 1;
-    float m_used = kNoKey, l = 0.f, pend = 1.0f;
+    // After an expired wait a warp skips further waits and work but still passes the named barriers.
     bool ok = true;
-    for (int i = 0; i < n_mine; ++i) {
-      const int t = two ? i : 2 * i + wg;
-      ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars[kBarSFull + wg], i & 1, limit));
-      if (!ok) break;
+    int n_s = 0, n_unit = 0;  // score tiles and units taken
+    while (walk.next(u)) {
+      const int tile0 = u.two ? wg * tpt : 0;  // this query tile's first token in the unit
+      const bool live = r < min(tpt, u.k.cnt - tile0) * G;
+      // how many of the part's keys this row sees; rows of no token see what the unit sees, so that
+      // they hold no whole warp on the masked path
+      const int seen = min(u.k.keys, p.causal && live ? u.k.place0 + tile0 + tok + 1 : u.k.keys) - u.j0;
+      const int n_mine = u.two ? u.n_tiles : (u.n_tiles + 1 - wg) >> 1;
+      float m_used = kNoKey, l = 0.f, pend = 1.0f;
+      for (int i = 0; i < n_mine; ++i, ++n_s) {
+        if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars[kBarSFull + wg], n_s & 1, limit));
+        if (!ok) continue;
+        ptx::tc_fence_after();
+        softmax_tile(i == 0, seen - (u.two ? i : 2 * i + wg) * kBN, tS, tO, sl2, c2, m_used, l, pend);
+        ptx::tmem_st_wait();
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(&bars[kBarPFull + wg]);
+      }
+      if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars[kBarODone], n_unit & 1, limit));
+      ++n_unit;
       ptx::tc_fence_after();
-      softmax_tile(i == 0, min(j1, last + 1) - j0 - t * kBN, tS, tO, sl2, c2, m_used, l, pend);
-      ptx::tmem_st_wait();
-      ptx::tc_fence_before();
-      ptx::mbar_arrive(&bars[kBarPFull + wg]);
-    }
-    if (ok && n_tiles > 0) ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars[kBarODone], 0, limit));
-    if (!ok && lane == 0) paged_report(w, kStatusTimeout);
-    ptx::tc_fence_after();
-    l *= pend;
-    float f = pend, fo = 0.f;  // factors of this warpgroup's O and of the other's
-    float* other = reinterpret_cast<float*>(smem) + r * kPartRow;
-    if (!two) {
-      // join the chains: the odd tiles' row goes through shared memory, free by now
-      if (wg == 1) {
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          uint32_t rr[32];
-          ptx::tmem_ld32(tO + 32 * c, rr);
-#pragma unroll
-          for (int v = 0; v < 8; ++v)
-            reinterpret_cast<float4*>(other + 32 * c)[v] =
-                n_mine == 0 ? make_float4(0.f, 0.f, 0.f, 0.f)
-                            : make_float4(__uint_as_float(rr[4 * v]), __uint_as_float(rr[4 * v + 1]),
-                                          __uint_as_float(rr[4 * v + 2]), __uint_as_float(rr[4 * v + 3]));
-        }
-        reinterpret_cast<float4*>(other + 128)[0] = make_float4(m_used, l, pend, 0.f);
-      }
-      ptx::named_bar_sync(1, 256);
-      if (wg == 0) {
-        const float4 e = reinterpret_cast<const float4*>(other + 128)[0];
-        const float m = fmaxf(m_used, e.x);
-        const float fa = ptx::ex2(m_used - m), fb = ptx::ex2(e.x - m);
-        f = pend * fa;
-        fo = e.z * fb;
-        l = l * fa + e.y * fb;
+      l *= pend;
+      float f0 = pend, f1 = 0.f;  // factors of the row's accumulator, and of the other chain's
+      bool has1 = false;
+      if (!u.two) {
+        // join the chains: both warpgroups see both accumulators, and take half of the columns each
+        chain[wg * kBM + r] = make_float4(m_used, l, pend, 0.f);
+        ptx::named_bar_sync(1, 256);
+        const float4 a = chain[r], e = chain[kBM + r];
+        const float m = fmaxf(a.x, e.x);
+        const float fa = ptx::ex2(a.x - m), fe = ptx::ex2(e.x - m);
+        f0 = a.z * fa;
+        f1 = e.z * fe;
+        l = a.y * fa + e.y * fe;
         m_used = m;
+        has1 = u.n_tiles > 1;
       }
-    }
-    if (ok && (two || wg == 0)) {
-      const long long row = q.q0 + i0 + tile0 + tok;
-      const int head = h * G + r - tok * G;
-      const long long rh = row * p.q_heads + head;
-      const bool parts = p.n_split > 1;
-      const float inv = parts ? 1.0f : (l > 0.f ? 1.0f / l : 0.f);
-      const long long at = static_cast<long long>(sp) * w.n_rows * p.q_heads + rh;
+      const long long row = u.k.row0 + tile0 + tok;
+      const int head = u.h * G + r - tok * G;
+      const bool whole = u.t0 == 0 && u.t1 == u.k.tiles;
+      const float inv = l == 0.f ? 0.f : 1.0f / l;  // a row that saw nothing: its accumulator may hold anything
+      const long long at = static_cast<long long>(u.slot) * kPagedPartRows + (u.two ? wg * kBM : 0) + r;  // of a part
 #pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
+      for (int c = u.two ? 0 : 2 * wg; ok && c < (u.two ? 4 : 2 * wg + 2); ++c) {
         uint32_t rr[32];
-        ptx::tmem_ld32(tO + 32 * c, rr);
+        ptx::tmem_ld32(lane_base + col_o(u.two ? wg : 0) + 32 * c, rr);
         float x[32];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) x[i] = n_tiles > 0 ? __uint_as_float(rr[i]) * f : 0.f;
-        if (!two) {
+        for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(rr[i]) * f0;
+        if (has1) {
+          ptx::tmem_ld32(lane_base + col_o(1) + 32 * c, rr);
 #pragma unroll
-          for (int v = 0; v < 8; ++v) {
-            const float4 y = reinterpret_cast<const float4*>(other + 32 * c)[v];
-            x[4 * v] += y.x * fo;
-            x[4 * v + 1] += y.y * fo;
-            x[4 * v + 2] += y.z * fo;
-            x[4 * v + 3] += y.w * fo;
-          }
+          for (int i = 0; i < 32; ++i) x[i] += __uint_as_float(rr[i]) * f1;
         }
         if (!live) continue;
-        if (parts) {
-          float4* dst = reinterpret_cast<float4*>(p.part + at * kHeadDim + 32 * c);
-#pragma unroll
-          for (int v = 0; v < 8; ++v) dst[v] = make_float4(x[4 * v], x[4 * v + 1], x[4 * v + 2], x[4 * v + 3]);
-        } else {
+        if (whole) {
           uint32_t ob[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) ob[i] = pack_bf16x2(x[2 * i] * inv, x[2 * i + 1] * inv);
+          for (int i = 0; i < 16; ++i)
+            ob[i] = l != 0.f ? pack_bf16x2(x[2 * i] * inv, x[2 * i + 1] * inv) : 0u;
           uint4* dst = reinterpret_cast<uint4*>(p.out + row * p.out_stride + head * kHeadDim + 32 * c);
 #pragma unroll
           for (int v = 0; v < 4; ++v) dst[v] = make_uint4(ob[4 * v], ob[4 * v + 1], ob[4 * v + 2], ob[4 * v + 3]);
+        } else {
+          float4* dst = reinterpret_cast<float4*>(p.part + at * kHeadDim + 32 * c);
+#pragma unroll
+          for (int v = 0; v < 8; ++v) dst[v] = make_float4(x[4 * v], x[4 * v + 1], x[4 * v + 2], x[4 * v + 3]);
         }
       }
-      if (live && parts) {
-        p.part_ml[at] = make_float2(m_used, l);
-      } else if (live) {
-        const float z = l > 0.f ? m_used + log2f(l) : -INFINITY;
-        if (p.lse != nullptr) p.lse[rh] = z * kLn2;
-        if (p.lse2 != nullptr) p.lse2[rh] = z;
+      if (ok && live && (u.two || wg == 0)) {
+        if (!whole) {
+          p.part_ml[at] = make_float2(m_used, l);
+        } else {
+          const float z = l > 0.f ? m_used + log2f(l) : l == 0.f ? -INFINITY : l;
+          const long long rh = row * p.q_heads + head;
+          if (p.lse != nullptr) p.lse[rh] = z * kLn2;
+          if (p.lse2 != nullptr) p.lse2[rh] = z;
+        }
+      }
+      // neither chain's next product may overwrite an accumulator that the other still reads
+      if (!u.two) {
+        ptx::tc_fence_before();
+        ptx::named_bar_sync(1, 256);
       }
     }
+    if (!ok && lane == 0) paged_report(w, kStatusTimeout);
   }
 
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
   if (warp == 9) ptx::tmem_dealloc(tmem, 512);
+}
+
+// ---------------------------------------------------------------- units that were shared
+// Work shared in a row: the unit that the start of share c cuts, if it is the first border inside that
+// unit; its parts are the second slot of thread block c - 1, then the first slots of c, c + 1, ... as far
+// as the unit goes. In step: the c-th of the last units; its first part, then the helpers', in
+// consecutive slots. One warp per row, in the order of the parts.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinSlices = kPagedPartRows / (kJoinThreads / 32) / 2;  // two rows per warp
+
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ PagedAttnParams p) {
+  const PagedView& w = p.view;
+  const int c = blockIdx.x / kJoinSlices, slice = blockIdx.x % kJoinSlices;
+  const PagedWork& work = *p.work;
+  int h, b, slot0, step, parts;
+  if (work.in_step) {
+    if (c >= work.n_tail) return;
+    const int left = work.rest[c + 1] - work.rest[c];
+    if (left == 0) return;
+    const int j0 = helper_of(work, work.rest[c]), j1 = helper_of(work, work.rest[c + 1] - 1);
+    const long long n = static_cast<long long>(work.waves) * kSmCount + c;
+    h = static_cast<int>(n / work.n_blocks);
+    b = static_cast<int>(n - static_cast<long long>(h) * work.n_blocks);
+    slot0 = 2 * c + j0;
+    step = 1;
+    parts = j1 - j0 + 2;
+  } else {
+    if (c == 0 || c >= work.n_ctas) return;
+    const long long x = share_start(work, w.kv_heads, c);
+    h = static_cast<int>(x / work.head_tiles);
+    const long long head0 = static_cast<long long>(h) * work.head_tiles;
+    b = find_block(p.blocks, work.n_blocks, static_cast<int>(x - head0));
+    const long long first = head0 + p.blocks[b].start, end = first + p.blocks[b].tiles;
+    if (x == first || share_start(work, w.kv_heads, c - 1) > first) return;  // no cut, or not the first
+    parts = 2;
+    while (c + parts - 1 < work.n_ctas && share_start(work, w.kv_heads, c + parts - 1) < end) ++parts;
+    slot0 = 2 * c - 1;
+    step = 2;
+  }
+  const PagedBlock k = p.blocks[b];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tpt = kBM / p.group;
+  for (int e = 0; e < 2; ++e) {
+    const int rr = (slice * 2 + e) * (kJoinThreads / 32) + warp;  // row of the unit
+    const int tile = rr / kBM, r = rr % kBM, tok = r / p.group;
+    if (r >= tpt * p.group || tile * tpt + tok >= k.cnt) continue;
+    auto slot = [&](int i) {
+      return static_cast<long long>(i == 0 ? slot0 : slot0 + 1 + (i - 1) * step) * kPagedPartRows + rr;
+    };
+    float m = kNoKey;
+    for (int i = lane; i < parts; i += 32) m = fmaxf(m, p.part_ml[slot(i)].x);
+    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    float l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+    for (int i = 0; i < parts; ++i) {
+      const float2 ml = p.part_ml[slot(i)];
+      const float4 y = *reinterpret_cast<const float4*>(p.part + slot(i) * kHeadDim + lane * 4);
+      const float f = ptx::ex2(ml.x - m);
+      l += ml.y * f;
+      o.x += y.x * f;
+      o.y += y.y * f;
+      o.z += y.z * f;
+      o.w += y.w * f;
+    }
+    const long long row = k.row0 + tile * tpt + tok;
+    const int head = h * p.group + r - tok * p.group;
+    const float inv = l == 0.f ? 0.f : 1.0f / l;
+    *reinterpret_cast<uint2*>(p.out + row * p.out_stride + head * kHeadDim + lane * 4) =
+        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    if (lane == 0) {
+      const float z = l > 0.f ? m + log2f(l) : l == 0.f ? -INFINITY : l;
+      const long long rh = row * p.q_heads + head;
+      if (p.lse != nullptr) p.lse[rh] = z * kLn2;
+      if (p.lse2 != nullptr) p.lse2[rh] = z;
+    }
+  }
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -806,8 +1132,9 @@ cudaError_t launch_paged_chunk(const CUtensorMap& tm_q, const CUtensorMap& tm_k,
                                const PagedAttnParams& p, cudaStream_t stream) {
   const cudaError_t err = configure();
   if (err != cudaSuccess) return err;
-  const unsigned grid = static_cast<unsigned>(p.n_blocks) * p.view.kv_heads * p.n_split;
-  paged_chunk_kernel<<<grid, kThreads, kSmemBytes, stream>>>(tm_q, tm_k, tm_v, p);
+  paged_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p);
+  paged_chunk_kernel<<<kSmCount, kThreads, kSmemBytes, stream>>>(tm_q, tm_k, tm_v, p);
+  paged_join_kernel<<<kSmCount * kJoinSlices, kJoinThreads, 0, stream>>>(p);
   return cudaGetLastError();
 }
 

@@ -85,11 +85,13 @@ int check_heads(const rkv_page_pool* pool, int q_heads, int n_rows) {
   return RKV_OK;
 }
 
-// How the call is cut up. Blocks of the single-token form take one (stream, KV head) each, two to an
-// SM; a key stream is split so that the batch, were every stream max_kv long, would give each SM's
-// two places four blocks (shorter streams then give fewer, never idle ones), but no shorter than
-// kMinSplit tokens, below which a block's fixed cost outweighs its share.
-constexpr int kSms = 148;
+// How the call is cut up.
+// Single-token form: a thread block takes one (stream, KV head), two to an SM; a key stream is split so that
+// the batch, were every stream max_kv long, would give each SM's two places four blocks (shorter
+// streams then give fewer, never idle ones), but no shorter than kMinSplit tokens, below which a
+// block's fixed cost outweighs its share.
+// Chunk form: one thread block per SM; they share the batch's key tiles evenly, whatever the lengths
+// (paged_plan_kernel).
 constexpr int kMinSplit = 256;
 
 rkv::PagedPlan plan_of(const rkv_page_pool* pool, const rkv_paged_batch* b, int q_heads, int n_rows, bool weight) {
@@ -97,31 +99,27 @@ rkv::PagedPlan plan_of(const rkv_page_pool* pool, const rkv_paged_batch* b, int 
   std::memset(&p, 0, sizeof(p));
   const int group = q_heads / pool->kv_heads;
   p.rows_form = static_cast<long long>(b->max_q) * group <= rkv::kPagedRows;
-  long long len = b->max_kv;
-  long long tile;
   if (p.rows_form) {
-    tile = rkv::kPagedDecodeTile;
     p.block_tokens = b->max_q > 0 ? b->max_q : 1;
     p.n_blocks = b->n_seqs;
     const long long blocks = static_cast<long long>(b->n_seqs) * pool->kv_heads;
-    const long long want = 8LL * kSms;
-    len = std::max<long long>((b->max_kv * blocks + want - 1) / want, kMinSplit);
+    const long long want = 8LL * rkv::kSmCount;
+    long long len = std::max<long long>((b->max_kv * blocks + want - 1) / want, kMinSplit);
+    len = std::max<long long>(len, (b->max_kv + rkv::kPagedMaxSplit - 1) / rkv::kPagedMaxSplit);
+    len = (len + rkv::kPagedDecodeTile - 1) / rkv::kPagedDecodeTile * rkv::kPagedDecodeTile;
+    p.split_keys = static_cast<int>(len);
+    p.n_split = std::max(1, static_cast<int>((b->max_kv + len - 1) / len));
   } else {
-    tile = rkv::kKeyBox;
     p.block_tokens = 2 * (rkv::kQueryBox / group);
     const long long per_seq = (static_cast<long long>(b->max_q) + p.block_tokens - 1) / p.block_tokens;
     p.n_blocks = static_cast<int>(std::min(static_cast<long long>(n_rows) / p.block_tokens + b->n_seqs,
                                            static_cast<long long>(b->n_seqs) * per_seq));
-    const long long blocks = static_cast<long long>(p.n_blocks) * pool->kv_heads;
-    if (blocks > 0 && blocks < kSms) {
-      const long long want = (kSms + blocks - 1) / blocks;
-      len = std::max<long long>((b->max_kv + want - 1) / want, 2 * kMinSplit);
+    // key tiles of one head are counted in 31 bits
+    if (static_cast<long long>(p.n_blocks) * (b->max_kv / rkv::kKeyBox + 1LL) >= (1LL << 31)) {
+      p.total = -1;
+      return p;
     }
   }
-  len = std::max<long long>(len, (b->max_kv + rkv::kPagedMaxSplit - 1) / rkv::kPagedMaxSplit);
-  len = std::max<long long>((len + tile - 1) / tile * tile, tile);
-  p.split_keys = static_cast<int>(len);
-  p.n_split = std::max(1, static_cast<int>((b->max_kv + len - 1) / len));
   const long long heads = static_cast<long long>(n_rows) * q_heads;
   auto take = [&p](long long bytes) {
     const long long at = p.total;
@@ -129,8 +127,18 @@ rkv::PagedPlan plan_of(const rkv_page_pool* pool, const rkv_paged_batch* b, int 
     return at;
   };
   p.lse = weight ? take(4 * heads) : -1;
-  p.part = p.n_split > 1 ? take(4 * heads * kHeadDim * p.n_split) : -1;
-  p.part_ml = p.n_split > 1 ? take(8 * heads * p.n_split) : -1;
+  p.part = p.part_ml = p.blocks = p.work = p.seq_first = -1;
+  if (p.rows_form && p.n_split > 1) {
+    p.part = take(4 * heads * kHeadDim * p.n_split);
+    p.part_ml = take(8 * heads * p.n_split);
+  } else if (!p.rows_form) {
+    const long long rows = 2LL * rkv::kSmCount * rkv::kPagedPartRows;
+    p.part = take(4 * rows * kHeadDim);
+    p.part_ml = take(8 * rows);
+    p.blocks = take(static_cast<long long>(sizeof(rkv::PagedBlock)) * p.n_blocks);
+    p.work = take(sizeof(rkv::PagedWork));
+    p.seq_first = take(4LL * b->n_seqs);
+  }
   p.score_stride = (b->max_kv + 63LL) / 64 * 64;
   p.scores = weight && p.rows_form ? take(4 * heads * p.score_stride) : -1;
   return p;
@@ -178,7 +186,9 @@ RKV_API int rkv_paged_workspace(const rkv_page_pool* pool, const rkv_paged_batch
   if (bytes == nullptr) return RKV_ERR_ARG;
   rc = check_heads(pool, q_heads, n_rows);
   if (rc) return rc;
-  *bytes = plan_of(pool, batch, q_heads, n_rows, with_weight != 0).total;
+  const long long total = plan_of(pool, batch, q_heads, n_rows, with_weight != 0).total;
+  if (total < 0) return RKV_ERR_UNSUPPORTED;
+  *bytes = total;
   return RKV_OK;
 }
 
@@ -197,6 +207,7 @@ RKV_API int rkv_paged_attention(const rkv_page_pool* pool, const rkv_paged_batch
       overlap(q, q_stride, out, out_stride, n_rows, q_heads))
     return RKV_ERR_ARG;
   const rkv::PagedPlan plan = plan_of(pool, batch, q_heads, n_rows, weight != nullptr);
+  if (plan.total < 0) return RKV_ERR_UNSUPPORTED;
   if (workspace_bytes < plan.total) return RKV_ERR_CAPACITY;
   if (plan.total > 0 && !aligned16(workspace)) return RKV_ERR_ARG;
   rkv::PagedAttnParams p;
@@ -217,6 +228,11 @@ RKV_API int rkv_paged_attention(const rkv_page_pool* pool, const rkv_paged_batch
   if (plan.lse >= 0) p.lse2 = reinterpret_cast<float*>(ws + plan.lse);
   if (plan.part >= 0) p.part = reinterpret_cast<float*>(ws + plan.part);
   if (plan.part_ml >= 0) p.part_ml = reinterpret_cast<float2*>(ws + plan.part_ml);
+  if (plan.blocks >= 0) {
+    p.blocks = reinterpret_cast<rkv::PagedBlock*>(ws + plan.blocks);
+    p.work = reinterpret_cast<rkv::PagedWork*>(ws + plan.work);
+    p.seq_first = reinterpret_cast<int*>(ws + plan.seq_first);
+  }
   if (plan.scores >= 0) p.scores = reinterpret_cast<float*>(ws + plan.scores);
   p.score_stride = plan.score_stride;
   p.block_tokens = plan.block_tokens;
@@ -238,7 +254,6 @@ RKV_API int rkv_paged_attention(const rkv_page_pool* pool, const rkv_paged_batch
                          rkv::kQueryBox / p.group))
       return RKV_ERR_CUDA;
     err = rkv::launch_paged_chunk(tm_q, tm_k, tm_v, p, st);
-    if (err == cudaSuccess && plan.n_split > 1) err = rkv::launch_paged_combine(p, st);
     if (err == cudaSuccess && weight != nullptr && batch->max_kv > 0) err = rkv::launch_paged_weight(tm_q, tm_k, p, st);
   }
   return cuda_rc(err);
