@@ -177,38 +177,52 @@ def flow_cfg_x0_renoise(xt, v_cond, v_uncond, eps, cfg_scale: float, sigma: floa
 
 
 # ---------------------------------------------------------------------- paged caches
-def _expect(ok: bool, where: str) -> None:
-    if not ok:
-        raise RkvError(ERR_ARG, where)
-
-
-def _tensor(t, dtype: str, shape, where: str, device=None):
-    """Check type, device and shape (None: any extent) of a torch tensor argument."""
-    ok = str(t.dtype) == "torch." + dtype and t.is_cuda and len(t.shape) == len(shape)
-    ok = ok and all(want is None or have == want for have, want in zip(t.shape, shape))
-    _expect(ok and (device is None or t.device == device), where)
-    return t
-
-
-def _rows_tensor(t, heads: int, rows, device, where: str):
-    """A [rows, heads, 128] bf16 tensor whose rows may lie apart; returns the row stride."""
-    _tensor(t, "bfloat16", (rows, heads, 128), where, device)
-    rows, row, head, one = t.shape[0], *t.stride()
-    _expect(one == 1 and (head == 128 or heads == 1), where)
-    return row if rows > 1 else heads * 128
-
-
-def _launch(fn, where: str, device, stream, *args) -> None:
-    """Call with the tensors' device current and, unless one is given, its current stream."""
+def _torch():
     import torch
+    return torch
+
+
+def _refuse(where: str):
+    raise RkvError(ERR_ARG, where)
+
+
+def _dense(t, dtype, shape, device, where: str):
+    """Pointer of a contiguous GPU tensor of this type and shape (None: any extent); refused otherwise."""
+    if (t.dtype is not dtype or not t.is_cuda or (device is not None and t.device != device) or t.dim() != len(shape)
+            or not t.is_contiguous()):
+        _refuse(where)
+    for have, want in zip(t.shape, shape):
+        if want is not None and have != want:
+            _refuse(where)
+    return t.data_ptr()
+
+
+def _rows(t, heads, rows, pool, where: str):
+    """(pointer, rows, heads, row stride) of a [rows, heads, 128] bf16 tensor whose rows may lie apart."""
+    if t.dtype is not pool.bf16 or t.dim() != 3 or t.device != pool.device:
+        _refuse(where)
+    n, h, d = t.shape
+    row, head, one = t.stride()
+    if (d != 128 or one != 1 or (head != 128 and h != 1) or (heads is not None and h != heads)
+            or (rows is not None and n != rows)):
+        _refuse(where)
+    return t.data_ptr(), n, h, row if n > 1 else h * 128
+
+
+def _launch(fn, where: str, pool, stream, *args) -> None:
+    """Call with the tensors' device current and, unless a stream is given, on its current stream."""
+    torch, index = pool.torch, pool.index
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    if torch.cuda.current_device() == device.index:
-        rc = fn(*args, _stream(stream))
+        stream = torch._C._cuda_getCurrentRawStream(index)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if torch._C._cuda_getDevice() == index:
+        rc = fn(*args, stream)
     else:
-        with torch.cuda.device(device):
-            rc = fn(*args, _stream(stream))
-    _check(rc, where)
+        with torch.cuda.device(index):
+            rc = fn(*args, stream)
+    if rc != OK:
+        _check(rc, where)
 
 
 class PagePool:
@@ -217,14 +231,20 @@ class PagePool:
 
     def __init__(self, k, v):
         where = "PagePool"
-        _tensor(k, "bfloat16", (None, None, None, 128), where)
-        _tensor(v, "bfloat16", k.shape, where, k.device)
+        torch = _torch()
+        if (k.dtype is not torch.bfloat16 or v.dtype is not torch.bfloat16 or not k.is_cuda or k.device != v.device
+                or k.dim() != 4 or k.shape != v.shape or k.shape[3] != 128):
+            _refuse(where)
         n, h, p, _ = k.shape
         for t in (k, v):
-            _expect(t.stride(3) == 1 and (p == 1 or t.stride(2) == 128) and (h == 1 or t.stride(1) == p * 128), where)
-        _expect(n == 1 or k.stride(0) == v.stride(0), where)
+            if t.stride(3) != 1 or (p > 1 and t.stride(2) != 128) or (h > 1 and t.stride(1) != p * 128):
+                _refuse(where)
+        if n > 1 and k.stride(0) != v.stride(0):
+            _refuse(where)
         self.k, self.v, self.device, self.kv_heads = k, v, k.device, h
+        self.torch, self.index, self.bf16 = torch, k.device.index, torch.bfloat16
         self._c = _PagePool(k.data_ptr(), v.data_ptr(), k.stride(0) if n > 1 else h * p * 128, n, h, p)
+        self._ref = ctypes.byref(self._c)
 
 
 class PagedBatch:
@@ -235,42 +255,44 @@ class PagedBatch:
 
     def __init__(self, page_table, kv_len, q_start, max_q: int, max_kv: int, status=None):
         where = "PagedBatch"
-        _tensor(page_table, "int32", (None, None), where)
+        i32 = _torch().int32
+        if page_table.dtype is not i32 or not page_table.is_cuda or page_table.dim() != 2:
+            _refuse(where)
         n, width = page_table.shape
         dev = page_table.device
-        _expect(page_table.stride(1) == 1 or width <= 1, where)
+        stride = page_table.stride(0) if n > 1 else width
+        if (width > 1 and page_table.stride(1) != 1) or stride < width:
+            _refuse(where)
         for t, shape in ((kv_len, (n,)), (q_start, (n + 1,)), (status, (1,))):
             if t is not None:
-                _tensor(t, "int32", shape, where, dev)
-                _expect(t.is_contiguous(), where)
-        stride = page_table.stride(0) if n > 1 else width
-        _expect(stride >= width, where)
+                _dense(t, i32, shape, dev, where)
         self.page_table, self.kv_len, self.q_start, self.status = page_table, kv_len, q_start, status
         self.device, self.n_seqs = dev, n
         self._c = _PagedBatch(_ptr(page_table), _ptr(kv_len), _ptr(q_start), _ptr(status), stride, n, max_q, max_kv)
+        self._ref = ctypes.byref(self._c)
 
     def poll(self, stream=None) -> int:
         """Synchronise the stream and return (and clear) the status: OK, ERR_PAGE or ERR_TIMEOUT."""
-        _expect(self.status is not None, "rkv_paged_poll_status")
-        import torch
-        with torch.cuda.device(self.device):
+        if self.status is None:
+            _refuse("rkv_paged_poll_status")
+        with _torch().cuda.device(self.device):
             return _lib.rkv_paged_poll_status(_ptr(self.status), _stream(stream))
 
 
 def paged_write(pool: PagePool, batch: PagedBatch, k, v, stream=None) -> None:
     """The chunk's K and V, [rows, kv_heads, 128] bf16, into the pages."""
     where = "rkv_paged_write"
-    _expect(pool.device == batch.device, where)
-    ks = _rows_tensor(k, pool.kv_heads, None, pool.device, where)
-    vs = _rows_tensor(v, pool.kv_heads, k.shape[0], pool.device, where)
-    _launch(_lib.rkv_paged_write, where, pool.device, stream, pool._c, batch._c, k.data_ptr(), v.data_ptr(),
-            k.shape[0], ks, vs)
+    if pool.device != batch.device:
+        _refuse(where)
+    kp, rows, _, ks = _rows(k, pool.kv_heads, None, pool, where)
+    vp, _, _, vs = _rows(v, pool.kv_heads, rows, pool, where)
+    _launch(_lib.rkv_paged_write, where, pool, stream, pool._ref, batch._ref, kp, vp, rows, ks, vs)
 
 
 def paged_workspace_bytes(pool: PagePool, batch: PagedBatch, rows: int, q_heads: int, weight: bool = False) -> int:
     """Bytes of workspace that ``paged_attention`` needs for a chunk tensor of ``rows`` rows."""
     n = _c_ll(0)
-    _check(_lib.rkv_paged_workspace(pool._c, batch._c, q_heads, rows, int(bool(weight)), ctypes.byref(n)),
+    _check(_lib.rkv_paged_workspace(pool._ref, batch._ref, q_heads, rows, int(bool(weight)), ctypes.byref(n)),
            "rkv_paged_workspace")
     return n.value
 
@@ -282,19 +304,19 @@ def paged_attention(pool: PagePool, batch: PagedBatch, q, out, causal: bool = Tr
     of every key, added up. ``workspace``: a uint8 tensor of ``paged_workspace_bytes`` (allocated on the
     call's stream if None)."""
     where = "rkv_paged_attention"
-    dev = pool.device
-    _expect(dev == batch.device and len(q.shape) == 3, where)
-    rows, heads = q.shape[0], q.shape[1]
-    qs = _rows_tensor(q, heads, None, dev, where)
-    os_ = _rows_tensor(out, heads, rows, dev, where)
-    if lse is not None:
-        _expect(_tensor(lse, "float32", (rows, heads), where, dev).is_contiguous(), where)
+    dev, torch = pool.device, pool.torch
+    if dev != batch.device:
+        _refuse(where)
+    qp, rows, heads, qs = _rows(q, None, None, pool, where)
+    op, _, _, os_ = _rows(out, heads, rows, pool, where)
+    zp = wp = None
     width = 0
+    if lse is not None:
+        zp = _dense(lse, torch.float32, (rows, heads), dev, where)
     if weight is not None:
-        _expect(_tensor(weight, "float32", (batch.n_seqs, pool.kv_heads, None), where, dev).is_contiguous(), where)
+        wp = _dense(weight, torch.float32, (batch.n_seqs, pool.kv_heads, None), dev, where)
         width = weight.shape[2]
     if workspace is None:
-        import torch
         size = paged_workspace_bytes(pool, batch, rows, heads, weight is not None)
         if stream is None:
             stream = torch.cuda.current_stream(dev)
@@ -302,11 +324,9 @@ def paged_attention(pool: PagePool, batch: PagedBatch, q, out, causal: bool = Tr
             stream = torch.cuda.ExternalStream(stream, dev) if stream else torch.cuda.default_stream(dev)
         with torch.cuda.stream(stream):
             workspace = torch.empty(size, dtype=torch.uint8, device=dev)
-    else:
-        _expect(_tensor(workspace, "uint8", (None,), where, dev).is_contiguous(), where)
-    _launch(_lib.rkv_paged_attention, where, dev, stream, pool._c, batch._c, q.data_ptr(), heads, rows, qs,
-            out.data_ptr(), os_, int(bool(causal)), _ptr(lse), _ptr(weight), width, workspace.data_ptr(),
-            workspace.shape[0])
+    sp = _dense(workspace, torch.uint8, (None,), dev, where)
+    _launch(_lib.rkv_paged_attention, where, pool, stream, pool._ref, batch._ref, qp, heads, rows, qs, op, os_,
+            1 if causal else 0, zp, wp, width, sp, workspace.shape[0])
 
 
 def paged_evict(pool: PagePool, batch: PagedBatch, weight, keep: int, sinks: int, recent: int, kept, kv_len_out,
@@ -315,13 +335,14 @@ def paged_evict(pool: PagePool, batch: PagedBatch, weight, keep: int, sinks: int
     in all, in their order. weight [n_seqs, kv_heads, tokens] fp32, kept [n_seqs, kv_heads, keep] int32 and
     kv_len_out [n_seqs] int32 (both written)."""
     where = "rkv_paged_evict"
-    dev, n = pool.device, batch.n_seqs
-    _expect(dev == batch.device, where)
-    for t, dtype, shape in ((weight, "float32", (n, pool.kv_heads, None)), (kept, "int32", (n, pool.kv_heads, keep)),
-                            (kv_len_out, "int32", (n,))):
-        _expect(_tensor(t, dtype, shape, where, dev).is_contiguous(), where)
-    _launch(_lib.rkv_paged_evict, where, dev, stream, pool._c, batch._c, weight.data_ptr(), weight.shape[2], keep,
-            sinks, recent, kept.data_ptr(), kv_len_out.data_ptr())
+    dev, n, torch = pool.device, batch.n_seqs, pool.torch
+    if dev != batch.device:
+        _refuse(where)
+    wp = _dense(weight, torch.float32, (n, pool.kv_heads, None), dev, where)
+    kp = _dense(kept, torch.int32, (n, pool.kv_heads, keep), dev, where)
+    lp = _dense(kv_len_out, torch.int32, (n,), dev, where)
+    _launch(_lib.rkv_paged_evict, where, pool, stream, pool._ref, batch._ref, wp, weight.shape[2], keep, sinks,
+            recent, kp, lp)
 
 
 class RollingKV:

@@ -2,9 +2,29 @@
 // checked lengths of a stream, the address of a cached token.
 #pragma once
 
+#include <utility>
+
 #include "rkv_internal.h"
 
 namespace rkv {
+
+// Launch a kernel of a call's chain that may be set up while the one before it still runs; it
+// waits for that one's results itself (ptx::wait_previous, in every thread block).
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t stream,
+                         A&&... args) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+}
 
 __device__ __forceinline__ void paged_report(const PagedView& w, unsigned bits) {
   if (w.status != nullptr) atomicOr(w.status, bits);

@@ -85,6 +85,7 @@ __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(const __grid_
   const int rank = blockIdx.x % size, sh = blockIdx.x / size;
   const int s = sh / w.kv_heads;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  ptx::let_next_launch();
   const int n = __ldg(w.kv_len + s);
   int* kept = p.kept + static_cast<long long>(sh) * p.keep;
   const bool bad = n < 0 || n > w.max_kv;
@@ -253,8 +254,8 @@ __device__ __forceinline__ MoveList move_list(const int* kept, int keep) {
   while (lo0 < hi0 || lo1 < hi1) {
     const int step0 = (hi0 - lo0 + kMoveThreads - 1) / kMoveThreads, step1 = (hi1 - lo1 + kMoveThreads - 1) / kMoveThreads;
     const int i0 = lo0 + t * step0, i1 = lo1 + t * step1;
-    const bool there = step0 > 0 && i0 < hi0 && __ldg(kept + i0) >= 0;
-    const bool stays = step1 > 0 && i1 < hi1 && __ldg(kept + i1) == i1;
+    const bool there = step0 > 0 && i0 < hi0 && kept[i0] >= 0;
+    const bool stays = step1 > 0 && i1 < hi1 && kept[i1] == i1;
     const int c0 = __syncthreads_count(there), c1 = __syncthreads_count(stays);
     // c probes hold: the border lies behind the last of them, up to the next probe
     hi0 = c0 == 0 ? lo0 : min(hi0, lo0 + c0 * step0);
@@ -282,6 +283,7 @@ __global__ void __launch_bounds__(kMoveThreads) paged_move_kernel(const __grid_c
   const int task = blockIdx.x / size / heads, b = blockIdx.x / size % heads;
   const int h = b % w.kv_heads, s = b / w.kv_heads;
   const int* kept = p.kept + static_cast<long long>(b) * p.keep;
+  ptx::wait_previous();
   const MoveList m = move_list(kept, p.keep);
   if (task == 2 * kMoveParts) {
     if (rank != 0) return;
@@ -292,7 +294,7 @@ __global__ void __launch_bounds__(kMoveThreads) paged_move_kernel(const __grid_c
 #pragma unroll
       for (int t = 0; t < 8; ++t) {
         const int i = i0 + t * kMoveThreads + threadIdx.x;
-        if (i < m.count) x[t] = wt[__ldg(kept + i)];
+        if (i < m.count) x[t] = wt[kept[i]];
       }
       __syncthreads();
 #pragma unroll
@@ -317,7 +319,7 @@ __global__ void __launch_bounds__(kMoveThreads) paged_move_kernel(const __grid_c
   };
   auto entry = [&](int tile, int t) {
     const int i = place(tile, t);
-    return i < m.count ? __ldg(kept + i) : -1;
+    return i < m.count ? kept[i] : -1;
   };
   // the list's raw entry (-1 where there is no token): checked where it is used, a whole tile after
   // its load was issued
@@ -425,15 +427,17 @@ cudaError_t launch_paged_evict(const PagedEvictParams& p, cudaStream_t stream) {
   const bool held = run <= 32 * kHeldKeys;
   cudaError_t err = configure();
   if (err != cudaSuccess) return err;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = size;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = size;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // for the second kernel
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(heads * size);
   cfg.blockDim = dim3(kSelThreads);
   cfg.stream = stream;
-  cfg.attrs = &attr;
+  cfg.attrs = attr;
   cfg.numAttrs = 1;
   err = held ? cudaLaunchKernelEx(&cfg, paged_select_kernel<true>, p)
              : cudaLaunchKernelEx(&cfg, paged_select_kernel<false>, p);
@@ -441,7 +445,8 @@ cudaError_t launch_paged_evict(const PagedEvictParams& p, cudaStream_t stream) {
   // blocks that share a column: up to eight, while the grid stays near three blocks to an SM
   size = kMoveCluster;
   while (size > 1 && heads * 2 * kMoveParts * size > 1024) size /= 2;
-  attr.val.clusterDim.x = size;
+  attr[0].val.clusterDim.x = size;
+  cfg.numAttrs = 2;
   cfg.gridDim = dim3(heads * (2 * kMoveParts + 1) * size);
   cfg.blockDim = dim3(kMoveThreads);
   cfg.dynamicSmemBytes = kMoveSmem;

@@ -95,6 +95,7 @@ __device__ __forceinline__ int plan_scan(int x, int* warp_sums, int& total) {
 // One thread block: the units of the batch and their key tiles, from the lengths on the device.
 __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_constant__ PagedAttnParams p) {
   __shared__ int warp_sums[32];
+  ptx::let_next_launch();
   const PagedView& w = p.view;
   const int t = threadIdx.x;
   int blocks = 0;
@@ -303,58 +304,20 @@ struct PagedWalk {
   }
 };
 
-// 2^x on the FMA pipe for two lanes: r = round(x) by adding 1.5 * 2^23, f = x - r in [-1/2, 1/2], a
-// polynomial for 2^f fitted for least relative error (tests/exp2_poly.py; degree 4: 2.7e-6, mean
-// 4e-8, which keeps a row sum within fp32's own rounding; degree 5: 2.3e-7), r added to the exponent.
-// x is clamped to [-125, 126].
-template <int kDegree>
-__device__ __forceinline__ void exp2_poly(uint64_t x2, float& y0, float& y1) {
-  float x0, x1;
-  ptx::f2_unpack(x2, x0, x1);
-  const uint64_t x = ptx::f2_pack(fminf(fmaxf(x0, -125.0f), 126.0f), fminf(fmaxf(x1, -125.0f), 126.0f));
-  const uint64_t t = ptx::f2_add(x, ptx::f2_pack(12582912.0f, 12582912.0f));
-  const uint64_t r = ptx::f2_add(t, ptx::f2_pack(-12582912.0f, -12582912.0f));
-  const uint64_t f = ptx::f2_fma(r, ptx::f2_pack(-1.0f, -1.0f), x);
-  auto two = [](float c) { return ptx::f2_pack(c, c); };
-  uint64_t q;
-  if (kDegree == 5) {
-    q = ptx::f2_fma(two(0.0013276471519076234f), f, two(0.00967554133066553f));
-    q = ptx::f2_fma(q, f, two(0.05550713274962234f));
-    q = ptx::f2_fma(q, f, two(0.24022119723934193f));
-    q = ptx::f2_fma(q, f, two(0.693146967063863f));
-    q = ptx::f2_fma(q, f, two(1.000000071654653f));
-  } else {
-    q = ptx::f2_fma(two(0.009570101434034835f), f, two(0.055917860281963716f));
-    q = ptx::f2_fma(q, f, two(0.2402474483964632f));
-    q = ptx::f2_fma(q, f, two(0.6931218147436669f));
-    q = ptx::f2_fma(q, f, two(0.9999992614421643f));
-  }
-  float t0, t1, q0, q1;
-  ptx::f2_unpack(t, t0, t1);
-  ptx::f2_unpack(q, q0, q1);
-  y0 = __uint_as_float((__float_as_uint(t0) << 23) + __float_as_uint(q0));
-  y1 = __uint_as_float((__float_as_uint(t1) << 23) + __float_as_uint(q1));
-}
-
-constexpr int kPolyPairs = 2;  // of every 8 pairs of an unmasked tile
-
 // 64 numerators 2^(s sl2 - m) of one row, packed to bf16 pairs (the operand type of the product
-// with V; half a step, 2^-8, of each), their unrounded sum in acc.
-template <bool kPoly>
+// with V; half a step, 2^-8, of each), their unrounded sum in acc. All on the special-function unit: a
+// polynomial for two pairs in eight, as in the rolling-window kernel, made the kernel 3 % slower (1046 us
+// against 1010 us, 2048 rows of 32 heads on 30720 cached tokens), its own degree 4 instead of 3 (a row sum
+// has to hold fp32) costing more issue slots than the unit gains.
 __device__ __forceinline__ void numerators(const uint32_t* sh, uint64_t c2, uint64_t nm2, uint32_t* pk,
                                            uint64_t (&acc)[4]) {
 #pragma unroll
   for (int k = 0; k < kBN / 4; ++k) {
     const uint64_t x = ptx::f2_fma(ptx::f2_pack(__uint_as_float(sh[2 * k]), __uint_as_float(sh[2 * k + 1])), c2, nm2);
     float a, b;
-    if (kPoly && (k & 7) < kPolyPairs) {
-      exp2_poly<4>(x, a, b);
-    } else {
-      float x0, x1;
-      ptx::f2_unpack(x, x0, x1);
-      a = ptx::ex2(x0);
-      b = ptx::ex2(x1);
-    }
+    ptx::f2_unpack(x, a, b);
+    a = ptx::ex2(a);
+    b = ptx::ex2(b);
     acc[k & 3] = ptx::f2_add(acc[k & 3], ptx::f2_pack(a, b));
     pk[k] = pack_bf16x2(a, b);
   }
@@ -389,12 +352,12 @@ __device__ __forceinline__ void softmax_tile(bool first, int valid, uint32_t tS,
       uint32_t sh[kBN / 2];
       ptx::tmem_ld64(tS + 64 * hh, sh);
       if (whole) {
-        numerators<true>(sh, c2, nm2, pk + 32 * hh, acc);
+        numerators(sh, c2, nm2, pk + 32 * hh, acc);
       } else {
 #pragma unroll
         for (int i = 0; i < kBN / 2; ++i)
           if (64 * hh + i >= valid) sh[i] = 0xff800000u;
-        numerators<false>(sh, c2, nm2, pk + 32 * hh, acc);
+        numerators(sh, c2, nm2, pk + 32 * hh, acc);
       }
     }
     const float lt = sum_of(acc);
@@ -445,12 +408,12 @@ __device__ __forceinline__ void softmax_tile(bool first, int valid, uint32_t tS,
       uint32_t sh[kBN / 2], pk[kBN / 4];
       ptx::tmem_ld64(tS + 64 * hh, sh);
       if (whole) {
-        numerators<true>(sh, c2, nm2, pk, acc);
+        numerators(sh, c2, nm2, pk, acc);
       } else {
 #pragma unroll
         for (int i = 0; i < kBN / 2; ++i)
           if (64 * hh + i >= valid) sh[i] = 0xff800000u;
-        numerators<false>(sh, c2, nm2, pk, acc);
+        numerators(sh, c2, nm2, pk, acc);
       }
       ptx::tmem_st32(tS + 32 * hh, pk);
     }
@@ -471,6 +434,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const unsigned long long limit = p.wait_limit_ns;
 
+  ptx::let_next_launch();
+  ptx::wait_previous();
   const PagedWork& work = *p.work;
   const int cta = blockIdx.x;
   if (cta >= work.n_ctas) return;
@@ -828,6 +793,8 @@ constexpr int kJoinThreads = 256;
 constexpr int kJoinSlices = kPagedPartRows / (kJoinThreads / 32) / 2;  // two rows per warp
 
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ PagedAttnParams p) {
+  ptx::let_next_launch();
+  ptx::wait_previous();
   const PagedView& w = p.view;
   const int c = blockIdx.x / kJoinSlices, slice = blockIdx.x % kJoinSlices;
   const PagedWork& work = *p.work;
@@ -899,30 +866,32 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
 // ---------------------------------------------------------------------------------------------
 // Attention weight of chunks. With z the rows' log-sum-exp from the attention before, key j of KV
 // head h gathers sum over the group's rows i that see it of 2^(s_ij - z_i). The product is
-// taken transposed, S^T = K Q^T: a block owns 128 keys (the TMEM lanes) and walks the query tiles
-// (128 columns), so that a key's sum stays in one thread's registers: no atomics, a fixed order. The
-// two warpgroups take every second query tile and are added up at the end.
-//   warp 8: TMA producer (the K tile once, query tiles into four stages), warp 9: MMA issuer;
-//   four S buffers fill the TMEM, two per warpgroup, so the next product runs beside the exponentials,
-//   which bound the kernel: 128 x 128 of them per tile against 8 MMA steps.
-constexpr int kWStages = 4;
+// taken transposed, S^T = K Q^T: a thread block owns 128 keys (the TMEM lanes) and walks the query tiles
+// (128 columns), so that a key's sum stays in one thread's registers: no atomics, a fixed order.
+//   warps 0-7: two warpgroups, one key per thread, every second query tile each (their sums are added
+//   up at the end); warp 8: TMA producer (the K tile once, query tiles into two stages); warp 9: TMEM
+//   allocator and MMA issuer, one S buffer per warpgroup.
+// The exponentials bound it (128 x 128 per tile against 8 MMA steps: 1024 clocks at 16 a clock). Each is
+// one of a chain of short dependent instructions, so two thread blocks per SM take turns, sixteen such
+// warps; and a thread block needs some 10000 clocks besides (start, first tiles, end), which the other covers.
+constexpr int kWGroups = 2;
+constexpr int kWThreads = kWGroups * 128 + 64;
 constexpr int kWSmemQ = kTile;
-constexpr int kWSmemLse = kWSmemQ + kWStages * kTile;  // [4][128] floats: -z per row, by S buffer
-constexpr int kWSmemBar = kWSmemLse + kWStages * kBM * 4;
+constexpr int kWSmemLse = kWSmemQ + kWGroups * kTile;  // [group][2][128] floats: -z per row, two tiles
+constexpr int kWSmemBar = kWSmemLse + kWGroups * 2 * kBM * 4;
 constexpr int kWSmemBytes = kWSmemBar + 256 + 1024;
-constexpr int kWPolyPairs = 2;
 
 enum : int {
   kWbK = 0,
-  kWbQFull = 1,    // +stage
-  kWbQEmpty = 5,   // +stage
-  kWbSFull = 9,    // +buffer
-  kWbSEmpty = 13,  // +buffer
-  kWbDrain = 17,
-  kWbCount = 18
+  kWbQFull = 1,                        // +stage
+  kWbQEmpty = kWbQFull + kWGroups,     // +stage
+  kWbSFull = kWbQEmpty + kWGroups,     // +buffer
+  kWbSEmpty = kWbSFull + kWGroups,     // +buffer
+  kWbDrain = kWbSEmpty + kWGroups,
+  kWbCount
 };
 
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kWThreads, 2)
     paged_weight_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ PagedAttnParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -933,10 +902,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const PagedView& w = p.view;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const unsigned long long limit = p.wait_limit_ns;
-  const int n_kt = (w.max_kv + kBN - 1) / kBN;
-  const int kt = blockIdx.x % n_kt, sh = blockIdx.x / n_kt;
+  // streams of different chunk lengths side by side in the launch order, so that they share its end
+  const int n_kt = (w.max_kv + kBN - 1) / kBN, n_sh = w.n_seqs * w.kv_heads;
+  const int kt = n_kt - 1 - blockIdx.x / n_sh, sh = blockIdx.x % n_sh;
   const int h = sh % w.kv_heads, s = sh / w.kv_heads;
   const PagedSeq q = paged_seq(w, s);
+  ptx::wait_previous();  // every thread, before any leaves: the weights follow the attention, also for later calls
   const int j0 = kt * kBN;
   if (!q.ok || q.n_q == 0 || j0 >= q.kv) return;  // a bad length was reported by the attention
   const int G = p.group;
@@ -946,19 +917,41 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int qt0 = p.causal ? max(0, j0 - first_place) / tpt : 0;
   const int n_qt = (q.n_q + tpt - 1) / tpt - qt0;
 
-  if (threadIdx.x == 0) {
-    ptx::mbar_init(&bars[kWbK], 1);
-    for (int i = 0; i < kWStages; ++i) {
-      ptx::mbar_init(&bars[kWbQFull + i], 1);
-      ptx::mbar_init(&bars[kWbQEmpty + i], 1);
-      ptx::mbar_init(&bars[kWbSFull + i], 1);
-      ptx::mbar_init(&bars[kWbSEmpty + i], kBM);
+  if (warp == kWGroups * 4) {  // the first loads leave before the rest of the thread block is ready
+    if (lane == 0) {
+      ptx::mbar_init(&bars[kWbK], 1);
+      for (int i = 0; i < kWGroups; ++i) {
+        ptx::mbar_init(&bars[kWbQFull + i], 1);
+        ptx::mbar_init(&bars[kWbQEmpty + i], 1);
+        ptx::mbar_init(&bars[kWbSFull + i], 1);
+        ptx::mbar_init(&bars[kWbSEmpty + i], kBM);
+      }
+      ptx::mbar_init(&bars[kWbDrain], 1);
+      ptx::fence_mbar_init();
     }
-    ptx::mbar_init(&bars[kWbDrain], 1);
-    ptx::fence_mbar_init();
+    __syncwarp();
+    const int box = min(1 << w.page_shift, kBN);
+    const int n_box = kBN / box;
+    const int b = lane % n_box, c = lane / n_box;
+    const int j = j0 + b * box;
+    if (lane == 0) ptx::mbar_arrive_expect_tx(&bars[kWbK], (min(kBN, q.kv - j0) + box - 1) / box * box * 256);
+    __syncwarp();
+    if (c < 2 && j < q.kv)
+      ptx::tma_load_3d(smem + c * kSlab + b * box * 128, &tm_k, &bars[kWbK], c * 64,
+                       (h << w.page_shift) + (j & ((1 << w.page_shift) - 1)),
+                       max(0, paged_id(w, s, j >> w.page_shift)));
   }
-  if (warp == 9) {
-    ptx::tmem_alloc(tmem_slot, 512);
+  auto load_q = [&](int t) {
+    const int st = t % kWGroups;
+    ptx::mbar_arrive_expect_tx(&bars[kWbQFull + st], 2 * 128 * tpt * G);
+    for (int cc = 0; cc < 2; ++cc)
+      ptx::tma_load_3d(smem + kWSmemQ + st * kTile + cc * kSlab, &tm_q, &bars[kWbQFull + st], cc * 64, h * G,
+                       q.q0 + (qt0 + t) * tpt);
+  };
+  if (warp == kWGroups * 4 && lane == 0)
+    for (int t = 0; t < min(n_qt, kWGroups); ++t) load_q(t);
+  if (warp == kWGroups * 4 + 1) {
+    ptx::tmem_alloc(tmem_slot, kWGroups * 128);
     ptx::tmem_relinquish();
   }
   ptx::tc_fence_before();
@@ -966,48 +959,29 @@ __global__ void __launch_bounds__(kThreads, 1)
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp == 8) {
-    const int box = min(1 << w.page_shift, kBN);
-    const int n_box = kBN / box;
-    const int b = lane % n_box, c = lane / n_box;
-    const int j = j0 + b * box;
-    if (lane == 0) {
-      ptx::prefetch_tmap(&tm_q);
-      const int boxes = (min(kBN, q.kv - j0) + box - 1) / box;
-      ptx::mbar_arrive_expect_tx(&bars[kWbK], boxes * box * 256);
-    }
-    __syncwarp();
-    if (c < 2 && j < q.kv)
-      ptx::tma_load_3d(smem + c * kSlab + b * box * 128, &tm_k, &bars[kWbK], c * 64,
-                       (h << w.page_shift) + (j & ((1 << w.page_shift) - 1)),
-                       max(0, paged_id(w, s, j >> w.page_shift)));
-    __syncwarp();
+  if (warp == kWGroups * 4) {
     if (lane == 0) {
       bool ok = true;
-      int nq = 0;
-      for (int t = 0; t < n_qt; ++t) {
-        const int st = t % kWStages;
-        if (t >= kWStages && !ptx::mbar_wait(&bars[kWbQEmpty + st], (t / kWStages - 1) & 1, limit)) { ok = false; break; }
-        ptx::mbar_arrive_expect_tx(&bars[kWbQFull + st], 2 * 128 * tpt * G);
-        for (int cc = 0; cc < 2; ++cc)
-          ptx::tma_load_3d(smem + kWSmemQ + st * kTile + cc * kSlab, &tm_q, &bars[kWbQFull + st], cc * 64, h * G,
-                           q.q0 + (qt0 + t) * tpt);
+      int nq = min(n_qt, kWGroups);
+      for (int t = nq; t < n_qt; ++t) {
+        if (!ptx::mbar_wait(&bars[kWbQEmpty + t % kWGroups], (t / kWGroups - 1) & 1, limit)) { ok = false; break; }
+        load_q(t);
         nq = t + 1;
       }
       if (!ok) paged_report(w, kStatusTimeout);
       ptx::mbar_wait(&bars[kWbK], 0, kDrainNs);
-      for (int t = max(0, nq - kWStages); t < nq; ++t)
-        ptx::mbar_wait(&bars[kWbQFull + t % kWStages], (t / kWStages) & 1, kDrainNs);
+      for (int t = max(0, nq - kWGroups); t < nq; ++t)
+        ptx::mbar_wait(&bars[kWbQFull + t % kWGroups], (t / kWGroups) & 1, kDrainNs);
     }
     __syncwarp();
-  } else if (warp == 9) {
+  } else if (warp == kWGroups * 4 + 1) {
     if (lane == 0) {
       const uint32_t ka = ptx::smem_u32(smem);
       bool ok = ptx::mbar_wait(&bars[kWbK], 0, limit);
       for (int t = 0; ok && t < n_qt; ++t) {
-        const int st = t % kWStages;  // the query stage and the S buffer
-        if (!ptx::mbar_wait(&bars[kWbQFull + st], (t / kWStages) & 1, limit)) { ok = false; break; }
-        if (t >= kWStages && !ptx::mbar_wait(&bars[kWbSEmpty + st], (t / kWStages - 1) & 1, limit)) { ok = false; break; }
+        const int st = t % kWGroups;  // the query stage, the S buffer and the warpgroup
+        if (!ptx::mbar_wait(&bars[kWbQFull + st], (t / kWGroups) & 1, limit)) { ok = false; break; }
+        if (t >= kWGroups && !ptx::mbar_wait(&bars[kWbSEmpty + st], (t / kWGroups - 1) & 1, limit)) { ok = false; break; }
         ptx::tc_fence_after();
         const uint32_t qa = ptx::smem_u32(smem + kWSmemQ + st * kTile);
 #pragma unroll
@@ -1024,87 +998,81 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     const int wg = warp >> 2;
     const int r = threadIdx.x & 127;  // key of the tile, and the query row whose z this thread fetches
-    const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t tS = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + wg * 128;
     const uint64_t c2 = ptx::f2_pack(p.scale_log2, p.scale_log2);
-    // -z of row r of query tile t; rows of no token get -infinity, which makes their weight 0
-    // (their scores are finite or are masked below)
+    const int my_tok = r / G;
+    const float* z_of = p.lse2 + static_cast<long long>(q.q0) * p.q_heads + h * G + r - my_tok * G;
+    // -z of row r of query tile t; what rows of no token get is masked below
     auto fetch = [&](int t) -> float {
-      const int tok = (qt0 + t) * tpt + r / G;
-      if (t >= n_qt || r >= tpt * G || tok >= q.n_q) return -INFINITY;
-      return -p.lse2[static_cast<long long>(q.q0 + tok) * p.q_heads + h * G + r % G];
+      const int tok = (qt0 + t) * tpt + my_tok;
+      if (t >= n_qt || my_tok >= tpt || tok >= q.n_q) return 0.f;
+      return -*(z_of + static_cast<long long>(tok) * p.q_heads);
     };
     float next = fetch(wg);
+    float* to = p.weight + (static_cast<long long>(s) * w.kv_heads + h) * p.weight_stride + j0 + r;
+    const float old = wg == 0 && j0 + r < first_place ? *to : 0.f;  // the chunk's own keys start from zero
     uint64_t acc[4] = {0, 0, 0, 0};
     bool ok = true;
-    for (int t = wg; t < n_qt; t += 2) {
-      const int st = t % kWStages;
-      float* z = nz + st * kBM;
+    int n = 0;  // tiles taken
+    for (int t = wg; t < n_qt; t += kWGroups, ++n) {
+      float* z = nz + (wg * 2 + (n & 1)) * kBM;
       z[r] = next;
-      next = fetch(t + 2);
+      next = fetch(t + kWGroups);
       // rows [lo, hi) of this tile are of the chunk and see this thread's key
       const int tok0 = (qt0 + t) * tpt;
       const int hi = min(tpt, q.n_q - tok0) * G;
       const int lo = p.causal ? max(0, j0 + r - first_place - tok0) * G : 0;
       const bool whole = __all_sync(0xffffffffu, lo == 0 && hi == kBM);
-      if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars[kWbSFull + st], (t / kWStages) & 1, limit));
-      ptx::named_bar_sync(1 + wg, kBM);  // the warpgroup's z are in place (and the buffer before last was read)
+      if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars[kWbSFull + wg], n & 1, limit));
+      ptx::named_bar_sync(1 + wg, kBM);  // every row's z is in place; the readers of two tiles ago are past it
       if (!ok) continue;
       ptx::tc_fence_after();
 #pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        uint32_t sh_[64];
-        ptx::tmem_ld64(lane_base + st * 128 + hh * 64, sh_);
-        if (hh == 1) {
+      for (int part = 0; part < 4; ++part) {
+        uint32_t sv[32];
+        ptx::tmem_ld32(tS + part * 32, sv);
+        if (part == 3) {
           ptx::tc_fence_before();
-          ptx::mbar_arrive(&bars[kWbSEmpty + st]);
+          ptx::mbar_arrive(&bars[kWbSEmpty + wg]);
         }
-        const uint64_t* zz = reinterpret_cast<const uint64_t*>(z + hh * 64);
-        if (whole) {
+        const ulonglong2* zz = reinterpret_cast<const ulonglong2*>(z + part * 32);
 #pragma unroll
-          for (int k = 0; k < 32; ++k) {
+        for (int k = 0; k < 16; k += 2) {
+          const ulonglong2 z2 = zz[k >> 1];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
             const uint64_t x = ptx::f2_fma(
-                ptx::f2_pack(__uint_as_float(sh_[2 * k]), __uint_as_float(sh_[2 * k + 1])), c2, zz[k]);
-            float a, e;
-            if ((k & 7) < kWPolyPairs) {
-              exp2_poly<5>(x, a, e);
-            } else {
-              ptx::f2_unpack(x, a, e);
-              a = ptx::ex2(a);
-              e = ptx::ex2(e);
+                ptx::f2_pack(__uint_as_float(sv[2 * (k + e)]), __uint_as_float(sv[2 * (k + e) + 1])), c2, e ? z2.y : z2.x);
+            float a, b;
+            ptx::f2_unpack(x, a, b);
+            a = ptx::ex2(a);
+            b = ptx::ex2(b);
+            if (!whole) {
+              const int i = part * 32 + 2 * (k + e);
+              a = i >= lo && i < hi ? a : 0.f;
+              b = i + 1 >= lo && i + 1 < hi ? b : 0.f;
             }
-            acc[k & 3] = ptx::f2_add(acc[k & 3], ptx::f2_pack(a, e));
-          }
-        } else {
-#pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            const int i = hh * 64 + 2 * k;
-            float a, e;
-            ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(__uint_as_float(sh_[2 * k]), __uint_as_float(sh_[2 * k + 1])), c2,
-                                       zz[k]), a, e);
-            a = i >= lo && i < hi ? ptx::ex2(a) : 0.f;
-            e = i + 1 >= lo && i + 1 < hi ? ptx::ex2(e) : 0.f;
-            acc[k & 3] = ptx::f2_add(acc[k & 3], ptx::f2_pack(a, e));
+            acc[(k + e) & 3] = ptx::f2_add(acc[(k + e) & 3], ptx::f2_pack(a, b));
           }
         }
       }
     }
     if (!ok && lane == 0) paged_report(w, kStatusTimeout);
-    const float sum = sum_of(acc);
-    float* half = nz;  // the z of every tile have been read once both warpgroups are here
-    ptx::named_bar_sync(3, 256);
-    if (wg == 1) half[r] = sum;
-    ptx::named_bar_sync(3, 256);
-    const int j = j0 + r;
-    if (wg == 0 && ok && j < q.kv) {
-      float* to = p.weight + (static_cast<long long>(s) * w.kv_heads + h) * p.weight_stride + j;
-      *to = (j < first_place ? *to : 0.f) + (sum + half[r]);
+    // the warpgroups' sums of a key, in order
+    ptx::named_bar_sync(1 + kWGroups, kWGroups * kBM);  // every z was read
+    nz[wg * kBM + r] = sum_of(acc);
+    ptx::named_bar_sync(1 + kWGroups, kWGroups * kBM);
+    if (wg == 0 && ok && j0 + r < q.kv) {
+      float sum = nz[r];
+      for (int g = 1; g < kWGroups; ++g) sum += nz[g * kBM + r];
+      *to = old + sum;
     }
   }
 
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  if (warp == 9) ptx::tmem_dealloc(tmem, 512);
+  if (warp == kWGroups * 4 + 1) ptx::tmem_dealloc(tmem, kWGroups * 128);
 }
 
 // the dynamic shared-memory limit is a per-device setting: raised once on every device this process
@@ -1130,12 +1098,14 @@ cudaError_t configure() {
 
 cudaError_t launch_paged_chunk(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                                const PagedAttnParams& p, cudaStream_t stream) {
-  const cudaError_t err = configure();
+  cudaError_t err = configure();
   if (err != cudaSuccess) return err;
   paged_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p);
-  paged_chunk_kernel<<<kSmCount, kThreads, kSmemBytes, stream>>>(tm_q, tm_k, tm_v, p);
-  paged_join_kernel<<<kSmCount * kJoinSlices, kJoinThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  err = cudaGetLastError();
+  if (err == cudaSuccess)
+    err = launch_after(paged_chunk_kernel, kSmCount, kThreads, kSmemBytes, stream, tm_q, tm_k, tm_v, p);
+  if (err == cudaSuccess) err = launch_after(paged_join_kernel, kSmCount * kJoinSlices, kJoinThreads, 0, stream, p);
+  return err;
 }
 
 cudaError_t launch_paged_weight(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const PagedAttnParams& p,
@@ -1144,8 +1114,7 @@ cudaError_t launch_paged_weight(const CUtensorMap& tm_q, const CUtensorMap& tm_k
   if (err != cudaSuccess) return err;
   const unsigned n_kt = (p.view.max_kv + kBN - 1) / kBN;
   const unsigned grid = n_kt * p.view.n_seqs * p.view.kv_heads;
-  paged_weight_kernel<<<grid, kThreads, kWSmemBytes, stream>>>(tm_q, tm_k, p);
-  return cudaGetLastError();
+  return launch_after(paged_weight_kernel, grid, kWThreads, kWSmemBytes, stream, tm_q, tm_k, p);
 }
 
 }  // namespace rkv

@@ -43,6 +43,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes);
   uint64_t* empty = full + kStages;
+  ptx::let_next_launch();
   const PagedView& w = p.view;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // blocks of one stream and head next to each other: they share pages' neighbourhoods in L2
@@ -324,10 +325,12 @@ __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const __
   const PagedView& w = p.view;
   const int head = blockIdx.x % p.q_heads, row = blockIdx.x / p.q_heads;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  ptx::let_next_launch();
   const int s = paged_seq_of_row(w, row);
-  if (s < 0) return;
-  const PagedSeq q = paged_seq(w, s);
-  if (!q.ok) return;
+  PagedSeq q = {};
+  if (s >= 0) q = paged_seq(w, s);
+  ptx::wait_previous();  // in every thread block, so that the kernel after this one may rely on it
+  if (s < 0 || !q.ok) return;
   // keys that the row's block of tokens sees, and so the parts that were written
   const int last_tok = min(q.n_q, ((row - q.q0) / p.block_tokens + 1) * p.block_tokens) - 1;
   const int keys = p.causal ? max(0, q.kv - q.n_q + last_tok + 1) : q.kv;
@@ -395,6 +398,7 @@ __global__ void __launch_bounds__(kTokenWeightThreads)
   const int h = sh % w.kv_heads, s = sh / w.kv_heads;
   const int j = (blockIdx.x - sh * n_kt) * kTokenWeightThreads + threadIdx.x;
   const PagedSeq q = paged_seq(w, s);
+  ptx::wait_previous();
   if (!q.ok || q.n_q == 0 || j >= q.kv) return;
   float sum = 0.f;
   for (int t = 0; t < q.n_q; ++t) {
@@ -411,8 +415,7 @@ __global__ void __launch_bounds__(kTokenWeightThreads)
 
 cudaError_t launch_paged_token_weight(const PagedAttnParams& p, cudaStream_t stream) {
   const unsigned n_kt = (p.view.max_kv + kTokenWeightThreads - 1) / kTokenWeightThreads;
-  paged_token_weight_kernel<<<n_kt * p.view.n_seqs * p.view.kv_heads, kTokenWeightThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_after(paged_token_weight_kernel, n_kt * p.view.n_seqs * p.view.kv_heads, kTokenWeightThreads, 0, stream, p);
 }
 
 cudaError_t launch_paged_decode(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const PagedAttnParams& p,
@@ -439,8 +442,7 @@ cudaError_t launch_paged_decode(const CUtensorMap& tm_k, const CUtensorMap& tm_v
 }
 
 cudaError_t launch_paged_combine(const PagedAttnParams& p, cudaStream_t stream) {
-  paged_combine_kernel<<<static_cast<unsigned>(p.view.n_rows) * p.q_heads, kCombineThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_after(paged_combine_kernel, static_cast<unsigned>(p.view.n_rows) * p.q_heads, kCombineThreads, 0, stream, p);
 }
 
 }  // namespace rkv
