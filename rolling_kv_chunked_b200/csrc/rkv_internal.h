@@ -149,16 +149,13 @@ struct PagedWriteParams {
 // How a call is cut up (a host rule on the batch's host values; workspace offsets in bytes).
 struct PagedPlan {
   int rows_form;     // 1: at most kPagedRows rows per stream and KV head, the form for single tokens
-  int block_tokens;  // chunk tokens of one block of rows
-  int split_keys;    // single-token form: cached tokens per part of a key stream
-  int n_split;       // and parts at most
-  int n_blocks;      // blocks of chunk tokens in the batch at most
-  long long lse, part, part_ml, scores, blocks, work, seq_first, total;  // -1: not used
+  int block_tokens;  // chunk form: tokens of one unit of rows
+  int n_blocks;      // and such units of one KV head in the batch at most
+  long long lse, part, part_ml, scores, cuts, blocks, work, seq_first, total;  // -1: not used
   long long score_stride;
 };
 
 constexpr int kPagedRows = 16;
-constexpr int kPagedMaxSplit = 256;
 
 // Work of the chunk form, laid out on the device by a small kernel from the lengths of the moment
 // (workspace). A block of up to block_tokens chunk tokens of one stream, for every KV head the same:
@@ -183,6 +180,10 @@ struct PagedWork {
   int waves, n_tail, quota;
   int rest[kSmCount + 1];  // in step: tiles left of the last units before unit i
 };
+// Single-token form: the unit that the start of a share cuts (n_q 0: none, or an earlier border cuts it).
+struct PagedCut {
+  int row0, n_q, h, parts;
+};
 constexpr int kPagedPartRows = 256;  // rows of a partial result of the chunk form
 
 struct PagedAttnParams {
@@ -196,15 +197,16 @@ struct PagedAttnParams {
   float scale_log2;  // log2(e) / sqrt(d)
   // workspace
   float* lse2;      // [n_rows][q_heads], log2; null when no weight is wanted
-  float* part;      // single-token form: [n_split][n_rows][q_heads][128], unnormalised sums of p v;
-                    // chunk form: [2 * kSmCount][kPagedPartRows][128]
+  float* part;      // unnormalised sums of p v of cut units: [4 * kSmCount][kPagedRows][128] (single-token
+                    // form) or [2 * kSmCount][kPagedPartRows][128]
   float2* part_ml;  // the same rows: reference (log2) and sum of p
+  PagedCut* cuts;      // single-token form: [2 * kSmCount]
   PagedBlock* blocks;  // chunk form: [n_blocks]
   PagedWork* work;
   int* seq_first;      // chunk form: [n_seqs], the stream's first block
   float* scores;    // [n_rows][q_heads][score_stride]: log2 scores of the single-token form; null: not kept
   long long score_stride;
-  int block_tokens, n_blocks, split_keys, n_split;
+  int block_tokens, n_blocks;
   unsigned long long wait_limit_ns;
 };
 
@@ -226,7 +228,6 @@ cudaError_t launch_paged_decode(const CUtensorMap& tm_k, const CUtensorMap& tm_v
 // min(page_tokens, kKeyBox) tokens.
 cudaError_t launch_paged_chunk(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                                const PagedAttnParams& p, cudaStream_t stream);
-cudaError_t launch_paged_combine(const PagedAttnParams& p, cudaStream_t stream);
 cudaError_t launch_paged_weight(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const PagedAttnParams& p,
                                 cudaStream_t stream);
 cudaError_t launch_paged_token_weight(const PagedAttnParams& p, cudaStream_t stream);

@@ -790,7 +790,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // as the unit goes. In step: the c-th of the last units; its first part, then the helpers', in
 // consecutive slots. One warp per row, in the order of the parts.
 constexpr int kJoinThreads = 256;
-constexpr int kJoinSlices = kPagedPartRows / (kJoinThreads / 32) / 2;  // two rows per warp
+constexpr int kJoinSlices = kPagedPartRows / (kJoinThreads / 32);  // a row per warp
 
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ PagedAttnParams p) {
   ptx::let_next_launch();
@@ -826,40 +826,35 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
   const PagedBlock k = p.blocks[b];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tpt = kBM / p.group;
-  for (int e = 0; e < 2; ++e) {
-    const int rr = (slice * 2 + e) * (kJoinThreads / 32) + warp;  // row of the unit
-    const int tile = rr / kBM, r = rr % kBM, tok = r / p.group;
-    if (r >= tpt * p.group || tile * tpt + tok >= k.cnt) continue;
-    auto slot = [&](int i) {
-      return static_cast<long long>(i == 0 ? slot0 : slot0 + 1 + (i - 1) * step) * kPagedPartRows + rr;
-    };
-    float m = kNoKey;
-    for (int i = lane; i < parts; i += 32) m = fmaxf(m, p.part_ml[slot(i)].x);
-    for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    float l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-    for (int i = 0; i < parts; ++i) {
-      const float2 ml = p.part_ml[slot(i)];
-      const float4 y = *reinterpret_cast<const float4*>(p.part + slot(i) * kHeadDim + lane * 4);
-      const float f = ptx::ex2(ml.x - m);
-      l += ml.y * f;
-      o.x += y.x * f;
-      o.y += y.y * f;
-      o.z += y.z * f;
-      o.w += y.w * f;
-    }
-    const long long row = k.row0 + tile * tpt + tok;
-    const int head = h * p.group + r - tok * p.group;
-    const float inv = l == 0.f ? 0.f : 1.0f / l;
-    *reinterpret_cast<uint2*>(p.out + row * p.out_stride + head * kHeadDim + lane * 4) =
-        make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-    if (lane == 0) {
-      const float z = l > 0.f ? m + log2f(l) : l == 0.f ? -INFINITY : l;
-      const long long rh = row * p.q_heads + head;
-      if (p.lse != nullptr) p.lse[rh] = z * kLn2;
-      if (p.lse2 != nullptr) p.lse2[rh] = z;
-    }
+  const int rr = slice * (kJoinThreads / 32) + warp;  // row of the unit
+  const int tile = rr / kBM, r = rr % kBM, tok = r / p.group;
+  if (r >= tpt * p.group || tile * tpt + tok >= k.cnt) return;
+  float m = kNoKey, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = 0; i < parts; ++i) {
+    const long long at = static_cast<long long>(i == 0 ? slot0 : slot0 + 1 + (i - 1) * step) * kPagedPartRows + rr;
+    const float2 e = p.part_ml[at];
+    const float4 y = *reinterpret_cast<const float4*>(p.part + at * kHeadDim + lane * 4);
+    const float mn = fmaxf(m, e.x);
+    const float f = ptx::ex2(m - mn), f2 = ptx::ex2(e.x - mn);
+    m = mn;
+    l = l * f + e.y * f2;
+    o.x = o.x * f + y.x * f2;
+    o.y = o.y * f + y.y * f2;
+    o.z = o.z * f + y.z * f2;
+    o.w = o.w * f + y.w * f2;
+  }
+  const long long row = k.row0 + tile * tpt + tok;
+  const int head = h * p.group + r - tok * p.group;
+  const float inv = l == 0.f ? 0.f : 1.0f / l;
+  *reinterpret_cast<uint2*>(p.out + row * p.out_stride + head * kHeadDim + lane * 4) =
+      make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+  if (lane == 0) {
+    const float z = l > 0.f ? m + log2f(l) : l == 0.f ? -INFINITY : l;
+    const long long rh = row * p.q_heads + head;
+    if (p.lse != nullptr) p.lse[rh] = z * kLn2;
+    if (p.lse2 != nullptr) p.lse2[rh] = z;
   }
 }
 

@@ -1,15 +1,21 @@
 // Attention over a paged cache when a stream brings few rows: at most 16 per KV head (a single
-// token of up to 16 grouped heads, a few drafted tokens of fewer). And the combine of parts, for
-// every form.
+// token of up to 16 grouped heads, a few drafted tokens of fewer).
 //
 // With R rows per KV head a cached token costs 512 bytes of K and V and 512 R multiply-adds, so
 // at 16 rows the memory asks for 16 flops a byte, a fraction of what even the warp-level matrix
 // instructions (mma.sync m16n8k16, whose 16 rows fit exactly) give: the kernel is bound by
-// HBM, and everything serves to keep loads in flight. A block takes one (stream, KV head, part
-// of the key stream); one warp issues TMA copies of 64-token tiles (K and V, one box per page and
-// 64-column half) into three stages, four warps own 16 tokens of each tile and run their own
-// softmax in registers, without meeting each other until the part's end, where the four partial
-// results are merged in shared memory. Two blocks fit an SM: six stages of 32 KB in flight.
+// HBM, and everything serves to keep loads in flight. One warp issues TMA copies of 64-token tiles (K
+// and V, one box per page and 64-column half) into three stages, four warps own 16 tokens of each tile and
+// run their own softmax in registers, without meeting each other until the unit's end, where the four
+// partial results are merged through shared memory. Two thread blocks fit an SM: six stages of 32 KB
+// in flight.
+//
+// A unit of work is one stream and KV head. Lengths differ, so all units' tiles, stream after stream and head
+// after head, are shared evenly by the 296 thread blocks that fit the card at once, each walking its share
+// without a pause at unit borders; units that a border cuts are left as partial rows for
+// paged_token_join_kernel. (Parts of a fixed length, a thread block each: 238 us for 48 streams of 49 to
+// 16384 tokens and 101 us for one of 131071 at the length that suits both, 221 and 91 us at the one that
+// suits each.) Every thread block counts the tiles for itself: one probe of 32 lengths per warp step.
 #include <mutex>
 
 #include "numeric.cuh"
@@ -25,7 +31,12 @@ constexpr int kStageBytes = 4 * kHalf;  // K halves, V halves
 constexpr int kStages = 3;
 constexpr int kWarps = 4;               // consumer warps, 16 tokens of a tile each
 constexpr int kDecodeThreads = (kWarps + 1) * 32;
-constexpr int kDecodeSmem = kStages * kStageBytes + 128 + 1024;
+constexpr int kMergeRows = kWarps;      // rows merged at a time, a warp each
+constexpr int kSmemMerge = kStages * kStageBytes;                              // [warp][row][128] floats
+constexpr int kSmemMl = kSmemMerge + kWarps * kMergeRows * kHeadDim * 4;       // [warp][row]: reference, sum
+constexpr int kSmemDecodeBar = kSmemMl + kWarps * 16 * 8;
+constexpr int kDecodeSmem = kSmemDecodeBar + 128 + 1024;
+constexpr int kMinTiles = 4;  // tiles of a share at least
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 8.0f;  // log2: the running reference follows a maximum only past this
 constexpr float kNoKey = -1e30f;  // reference (log2) of a row that has seen no key
@@ -36,31 +47,133 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// Tiles of one KV head of a stream: none without rows, one (all masked) if nothing is cached.
+__device__ __forceinline__ int seq_tiles(const PagedSeq& q) {
+  return q.ok && q.n_q > 0 ? max(1, (q.kv + kTileKeys - 1) / kTileKeys) : 0;
+}
+
+// A unit, or the part of one, of a thread block's share.
+struct TokenUnit {
+  PagedSeq q;
+  int s, h;
+  int t0, t1, tiles;  // its tiles, and the unit's
+};
+
+// x / y where both nearly always fit 32 bits (a 64-bit division is some 100 instructions).
+__device__ __forceinline__ long long quotient(long long x, int y) {
+  return (x >> 32) == 0 ? static_cast<long long>(static_cast<unsigned>(x) / static_cast<unsigned>(y)) : x / y;
+}
+
+// All tiles of the batch, and a place among them. Whole warps call these.
+struct TokenWalk {
+  long long each, left;  // tiles of a share (the first `more` shares have one more), tiles still to walk
+  int n, more;           // shares
+  int s, h, t;           // the place: stream, head, tile
+  PagedSeq q;
+  int tiles;
+  int q0, n_q, kv, mine;  // lane l: stream l of the first 32, and its tiles of one head
+
+  __device__ __forceinline__ void count(const PagedView& w) {
+    const int lane = threadIdx.x & 31;
+    long long all = 0;
+    for (int base = 0; base < w.n_seqs; base += 32) {
+      int x = 0;
+      if (base + lane < w.n_seqs) {
+        const PagedSeq y = paged_seq(w, base + lane);
+        if (!y.ok && blockIdx.x == 0) paged_report(w, kStatusLength);
+        x = seq_tiles(y);
+        if (base == 0) {
+          q0 = y.q0;
+          n_q = y.n_q;
+          kv = y.kv;
+        }
+      }
+      if (base == 0) mine = x;
+      all += __reduce_add_sync(0xffffffffu, x);
+    }
+    all *= w.kv_heads;
+    n = static_cast<int>(min(static_cast<long long>(2 * kSmCount), (all + kMinTiles - 1) / kMinTiles));
+    each = n > 0 ? quotient(all, n) : 0;
+    more = static_cast<int>(all - each * n);
+  }
+  __device__ __forceinline__ long long start(int c) const { return each * c + min(c, more); }
+  __device__ __forceinline__ void go_to(const PagedView& w, long long x) {
+    const int lane = threadIdx.x & 31;
+    long long before = 0;
+    for (int base = 0; base < w.n_seqs; base += 32) {
+      const int c = base == 0 ? mine : base + lane < w.n_seqs ? seq_tiles(paged_seq(w, base + lane)) : 0;
+      int inc = c;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, inc, d);
+        if (lane >= d) inc += y;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, (before + inc) * w.kv_heads > x);
+      if (hit) {
+        const int l = __ffs(hit) - 1;
+        s = base + l;
+        before += __shfl_sync(0xffffffffu, inc - c, l);
+        tiles = __shfl_sync(0xffffffffu, c, l);
+        if (base == 0) {
+          q.q0 = __shfl_sync(0xffffffffu, q0, l);
+          q.n_q = __shfl_sync(0xffffffffu, n_q, l);
+          q.kv = __shfl_sync(0xffffffffu, kv, l);
+          q.ok = true;
+        } else {
+          q = paged_seq(w, s);
+        }
+        break;
+      }
+      before += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    const long long in = x - before * w.kv_heads;
+    h = static_cast<int>(quotient(in, tiles));
+    t = static_cast<int>(in - static_cast<long long>(h) * tiles);
+  }
+  // What the join has to do where share c starts: nothing unless this is the first border inside a unit.
+  __device__ __forceinline__ PagedCut cut(int c) const {
+    PagedCut r = {};
+    const long long x = start(c), first = x - t, end = first + tiles;
+    if (t == 0 || start(c - 1) > first) return r;
+    r.row0 = q.q0;
+    r.n_q = q.n_q;
+    r.h = h;
+    r.parts = 2;
+    while (c + r.parts - 1 < n && start(c + r.parts - 1) < end) ++r.parts;
+    return r;
+  }
+  __device__ __forceinline__ bool next(const PagedView& w, TokenUnit& u) {
+    if (left <= 0) return false;
+    u.q = q;
+    u.s = s;
+    u.h = h;
+    u.t0 = t;
+    u.t1 = static_cast<int>(min(static_cast<long long>(tiles), t + left));
+    u.tiles = tiles;
+    left -= u.t1 - t;
+    t = 0;
+    if (++h == w.kv_heads && left > 0) {
+      h = 0;
+      do {
+        q = paged_seq(w, ++s);
+        tiles = seq_tiles(q);
+      } while (tiles == 0);
+    }
+    return true;
+  }
+};
+
 __global__ void __launch_bounds__(kDecodeThreads, 2)
     paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                         const __grid_constant__ PagedAttnParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kSmemDecodeBar);
   uint64_t* empty = full + kStages;
   ptx::let_next_launch();
   const PagedView& w = p.view;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // blocks of one stream and head next to each other: they share pages' neighbourhoods in L2
-  const int sp = blockIdx.x % p.n_split;
-  const int sh = blockIdx.x / p.n_split;
-  const int h = sh % w.kv_heads, s = sh / w.kv_heads;
-  const PagedSeq q = paged_seq(w, s);
-  if (!q.ok) {
-    if (threadIdx.x == 0) paged_report(w, kStatusLength);
-    return;
-  }
-  const int rows = q.n_q * p.group;
-  const int j0 = sp * p.split_keys;
-  if (rows == 0 || (j0 >= q.kv && (sp > 0 || p.n_split > 1))) return;
-  const int j1 = min(q.kv, j0 + p.split_keys);
-  const int n_tiles = (j1 - j0 + kTileKeys - 1) / kTileKeys;  // 0 only when kv == 0
-
+  const int cta = blockIdx.x;
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       ptx::mbar_init(&full[i], 1);
@@ -68,7 +181,17 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
     }
     ptx::fence_mbar_init();
   }
+  TokenWalk walk;
+  walk.count(w);
+  if (cta >= walk.n) {
+    if (threadIdx.x == 0) p.cuts[cta] = PagedCut{};
+    return;
+  }
+  walk.left = walk.start(cta + 1) - walk.start(cta);
+  walk.go_to(w, walk.start(cta));
+  if (threadIdx.x == 0) p.cuts[cta] = walk.cut(cta);
   __syncthreads();
+  TokenUnit u;
 
   if (warp == kWarps) {
     // ------------------------------------------------------------ TMA producer
@@ -78,307 +201,315 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
     const bool is_v = (lane / n_box) & 2;
     const bool mine = lane < 4 * n_box;
     const CUtensorMap* tm = is_v ? &tm_v : &tm_k;
-    const int dst = (is_v ? 2 : 0) * kHalf + c * kHalf + b * box * 128;
+    uint8_t* dst = smem + (is_v ? 2 : 0) * kHalf + c * kHalf + b * box * 128;
     if (mine && b == 0 && c == 0) ptx::prefetch_tmap(tm);
     bool ok = true;
-    int issued = 0;
-    int id = -1;
-    if (mine && j0 + b * box < j1) id = paged_id(w, s, (j0 + b * box) >> w.page_shift);
-    for (int t = 0; t < n_tiles; ++t) {
-      const int st = t % kStages;
-      const int j = j0 + t * kTileKeys + b * box;
-      const int page = id;
-      // the next tile's page, on its way while this tile's stage is waited for
-      if (mine && j + kTileKeys < j1) id = paged_id(w, s, (j + kTileKeys) >> w.page_shift);
-      if (t >= kStages) {
-        ok = ptx::mbar_wait(&empty[st], ((t / kStages) - 1) & 1, p.wait_limit_ns);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
+    int g = 0;  // tiles issued
+    while (ok && walk.next(w, u)) {
+      const int kv = u.q.kv;
+      int id = -1;
+      if (mine && u.t0 * kTileKeys + b * box < kv) id = paged_id(w, u.s, (u.t0 * kTileKeys + b * box) >> w.page_shift);
+      for (int t = u.t0; t < u.t1; ++t) {
+        const int st = g % kStages;
+        const int j = t * kTileKeys + b * box;
+        const int page = max(id, 0);
+        // the next tile's page, on its way while this tile's stage is waited for
+        if (mine && t + 1 < u.t1 && j + kTileKeys < kv) id = paged_id(w, u.s, (j + kTileKeys) >> w.page_shift);
+        if (g >= kStages) {
+          ok = __all_sync(0xffffffffu, ptx::mbar_wait(&empty[st], ((g / kStages) - 1) & 1, p.wait_limit_ns));
+          if (!ok) break;
+        }
+        if (lane == 0) {
+          const int boxes = (max(0, min(kv - t * kTileKeys, kTileKeys)) + box - 1) / box;
+          ptx::mbar_arrive_expect_tx(&full[st], boxes * box * 128 * 4);
+        }
+        __syncwarp();
+        if (mine && j < kv)
+          ptx::tma_load_3d(dst + st * kStageBytes, tm, &full[st], c * 64,
+                           (u.h << w.page_shift) + (j & ((1 << w.page_shift) - 1)), page);
+        ++g;
       }
-      if (lane == 0) {
-        const int boxes = (min(j1 - (j0 + t * kTileKeys), kTileKeys) + box - 1) / box;
-        ptx::mbar_arrive_expect_tx(&full[st], boxes * box * 128 * 4);
-      }
-      __syncwarp();
-      if (mine && j < j1)
-        ptx::tma_load_3d(smem + st * kStageBytes + dst, tm, &full[st], c * 64,
-                         (h << w.page_shift) + (j & ((1 << w.page_shift) - 1)), max(page, 0));
-      issued = t + 1;
     }
     if (!ok && lane == 0) paged_report(w, kStatusTimeout);
-    // every copy issued must land before the block may exit
+    // every copy issued must land before the thread block may exit
     if (lane == 0)
-      for (int t = max(0, issued - kStages); t < issued; ++t)
-        ptx::mbar_wait(&full[t % kStages], (t / kStages) & 1, kDrainNs);
+      for (int t = max(0, g - kStages); t < g; ++t) ptx::mbar_wait(&full[t % kStages], (t / kStages) & 1, kDrainNs);
     return;
   }
 
   // -------------------------------------------------------------- consumers
   const int ra = lane >> 2, rb = ra + 8;  // this lane's two rows
   const int cq = (lane & 3) * 2;          // and its pair of columns within 8
-  uint32_t qa[8][4];
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int r = e ? rb : ra;
-    const int tok = r / p.group;
-    const bool live = r < rows;
-    const uint16_t* src = p.q + (q.q0 + (live ? tok : 0)) * p.q_stride + (h * p.group + r - tok * p.group) * kHeadDim;
-#pragma unroll
-    for (int kk = 0; kk < 8; ++kk) {
-      qa[kk][e] = live ? __ldg(reinterpret_cast<const uint32_t*>(src + kk * 16 + cq)) : 0u;
-      qa[kk][2 + e] = live ? __ldg(reinterpret_cast<const uint32_t*>(src + kk * 16 + 8 + cq)) : 0u;
-    }
-  }
-  // the last place each row sees
-  const int last_a = p.causal ? q.kv - q.n_q + ra / p.group : q.kv - 1;
-  const int last_b = p.causal ? q.kv - q.n_q + rb / p.group : q.kv - 1;
-  const int last_all = p.causal ? q.kv - q.n_q : q.kv - 1;
-  // where their scores go (a pair of places each), if they are kept
-  auto score_row = [&](int r) {
-    return (static_cast<long long>(q.q0 + r / p.group) * p.q_heads + h * p.group + r % p.group) * p.score_stride + cq;
-  };
-  const long long score_a = score_row(ra), score_b = score_row(rb);
-  float o[16][4];
-#pragma unroll
-  for (int i = 0; i < 16; ++i)
-#pragma unroll
-    for (int c = 0; c < 4; ++c) o[i][c] = 0.f;
-  float ma = kNoKey, mb = kNoKey, la = 0.f, lb = 0.f;  // references (log2) and this lane's sums
+  const int tok_a = ra / p.group, tok_b = rb / p.group;
   // ldmatrix rows: K by token (lanes 8-15: the next 8 columns, 16-31: the next 8 tokens), V by token
   // (lanes 8-15: the next 8 tokens, 16-31: the next 8 columns)
   const int krow = warp * 16 + (lane >> 4) * 8 + (lane & 7), kcol = (lane >> 3) & 1;
   const int vrow = warp * 16 + ((lane >> 3) & 1) * 8 + (lane & 7), vcol = lane >> 4;
   const uint32_t sbase = ptx::smem_u32(smem);
-  bool ok = true;
-  for (int t = 0; t < n_tiles; ++t) {
-    const int st = t % kStages;
-    ok = ptx::mbar_wait(&full[st], (t / kStages) & 1, p.wait_limit_ns);
-    ok = __all_sync(0xffffffffu, ok);
-    if (!ok) break;
-    const uint32_t kt = sbase + st * kStageBytes, vt = kt + 2 * kHalf;
-    const int jw = j0 + t * kTileKeys + warp * 16;  // this warp's first token
-    if (jw < j1) {
-      float sc[2][4];
+  float* mo = reinterpret_cast<float*>(smem + kSmemMerge);
+  float2* ml = reinterpret_cast<float2*>(smem + kSmemMl);
+  bool ok = true;  // after an expired wait a warp skips further work but still passes the barriers
+  int g = 0;
+  while (walk.next(w, u)) {
+    const PagedSeq& q = u.q;
+    const int rows = q.n_q * p.group;
+    uint32_t qa[8][4];
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) sc[i][c] = 0.f;
+    for (int e = 0; e < 2; ++e) {
+      const int r = e ? rb : ra, tok = e ? tok_b : tok_a;
+      const bool live = r < rows;
+      const uint16_t* src = p.q + (q.q0 + (live ? tok : 0)) * p.q_stride + (u.h * p.group + r - tok * p.group) * kHeadDim;
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk) {
-        const int chunk = kk * 2 + kcol;  // 16-byte chunk of the row; 128-byte swizzle within a half
-        uint32_t b[4];
-        ptx::ldsm4(kt + (chunk >> 3) * kHalf + krow * 128 + (((chunk & 7) ^ (krow & 7)) << 4), b);
-        ptx::mma16816(sc[0], qa[kk], b[0], b[1]);
-        ptx::mma16816(sc[1], qa[kk], b[2], b[3]);
+        qa[kk][e] = live ? __ldg(reinterpret_cast<const uint32_t*>(src + kk * 16 + cq)) : 0u;
+        qa[kk][2 + e] = live ? __ldg(reinterpret_cast<const uint32_t*>(src + kk * 16 + 8 + cq)) : 0u;
       }
+    }
+    // the last place each row sees
+    const int last_a = p.causal ? q.kv - q.n_q + tok_a : q.kv - 1;
+    const int last_b = p.causal ? q.kv - q.n_q + tok_b : q.kv - 1;
+    const int last_all = p.causal ? q.kv - q.n_q : q.kv - 1;
+    // where their scores go (a pair of places each), if they are kept
+    const long long score_a = (static_cast<long long>(q.q0 + tok_a) * p.q_heads + u.h * p.group + ra - tok_a * p.group) * p.score_stride + cq;
+    const long long score_b = (static_cast<long long>(q.q0 + tok_b) * p.q_heads + u.h * p.group + rb - tok_b * p.group) * p.score_stride + cq;
+    float o[16][4];
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < 16; ++i)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) sc[i][c] *= p.scale_log2;
-      const bool ragged = jw + 15 > last_all;
-      if (ragged) {
+      for (int c = 0; c < 4; ++c) o[i][c] = 0.f;
+    float ma = kNoKey, mb = kNoKey, la = 0.f, lb = 0.f;  // references (log2) and this lane's sums
+    for (int t = u.t0; t < u.t1; ++t, ++g) {
+      const int st = g % kStages;
+      if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait(&full[st], (g / kStages) & 1, p.wait_limit_ns));
+      if (!ok) continue;
+      const uint32_t kt = sbase + st * kStageBytes, vt = kt + 2 * kHalf;
+      const int jw = t * kTileKeys + warp * 16;  // this warp's first token
+      if (jw < q.kv) {
+        // four chains of four products: the scores' latency is half the tile's
+        float sc[2][4], sd[2][4];
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            if (jw + i * 8 + cq + (c & 1) > (c < 2 ? last_a : last_b)) sc[i][c] = -INFINITY;
-      }
-      if (p.scores != nullptr) {
+          for (int c = 0; c < 4; ++c) sc[i][c] = sd[i][c] = 0.f;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          const int chunk = kk * 2 + kcol;  // 16-byte chunk of the row; 128-byte swizzle within a half
+          uint32_t b[4];
+          ptx::ldsm4(kt + (chunk >> 3) * kHalf + krow * 128 + (((chunk & 7) ^ (krow & 7)) << 4), b);
+          ptx::mma16816(kk & 1 ? sd[0] : sc[0], qa[kk], b[0], b[1]);
+          ptx::mma16816(kk & 1 ? sd[1] : sc[1], qa[kk], b[2], b[3]);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) sc[i][c] = (sc[i][c] + sd[i][c]) * p.scale_log2;
+        if (jw + 15 > last_all) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              if (jw + i * 8 + cq + (c & 1) > (c < 2 ? last_a : last_b)) sc[i][c] = -INFINITY;
+        }
+        if (p.scores != nullptr) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if (ra < rows)
+              *reinterpret_cast<float2*>(p.scores + score_a + jw + i * 8) = make_float2(sc[i][0], sc[i][1]);
+            if (rb < rows)
+              *reinterpret_cast<float2*>(p.scores + score_b + jw + i * 8) = make_float2(sc[i][2], sc[i][3]);
+          }
+        }
+        float xa = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));
+        float xb = fmaxf(fmaxf(sc[0][2], sc[0][3]), fmaxf(sc[1][2], sc[1][3]));
+        xa = fmaxf(xa, __shfl_xor_sync(0xffffffffu, xa, 1));
+        xb = fmaxf(xb, __shfl_xor_sync(0xffffffffu, xb, 1));
+        xa = fmaxf(xa, __shfl_xor_sync(0xffffffffu, xa, 2));
+        xb = fmaxf(xb, __shfl_xor_sync(0xffffffffu, xb, 2));
+        if (__any_sync(0xffffffffu, xa > ma + kRescale || xb > mb + kRescale)) {
+          const float na = fmaxf(ma, xa), nb = fmaxf(mb, xb);
+          const float fa = ptx::ex2(ma - na), fb = ptx::ex2(mb - nb);
+          ma = na;
+          mb = nb;
+          la *= fa;
+          lb *= fb;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            o[i][0] *= fa;
+            o[i][1] *= fa;
+            o[i][2] *= fb;
+            o[i][3] *= fb;
+          }
+        }
+        // p in fp32 for the sum; rounded to bf16 for the product with V, the operand type of the
+        // matrix instruction (half a step, 2^-8, of each weight: the size of the output's own rounding)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          if (ra < rows)
-            *reinterpret_cast<float2*>(p.scores + score_a + jw + i * 8) = make_float2(sc[i][0], sc[i][1]);
-          if (rb < rows)
-            *reinterpret_cast<float2*>(p.scores + score_b + jw + i * 8) = make_float2(sc[i][2], sc[i][3]);
+          sc[i][0] = ptx::ex2(sc[i][0] - ma);
+          sc[i][1] = ptx::ex2(sc[i][1] - ma);
+          sc[i][2] = ptx::ex2(sc[i][2] - mb);
+          sc[i][3] = ptx::ex2(sc[i][3] - mb);
+          la += sc[i][0] + sc[i][1];
+          lb += sc[i][2] + sc[i][3];
         }
-      }
-      float xa = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));
-      float xb = fmaxf(fmaxf(sc[0][2], sc[0][3]), fmaxf(sc[1][2], sc[1][3]));
-      xa = fmaxf(xa, __shfl_xor_sync(0xffffffffu, xa, 1));
-      xb = fmaxf(xb, __shfl_xor_sync(0xffffffffu, xb, 1));
-      xa = fmaxf(xa, __shfl_xor_sync(0xffffffffu, xa, 2));
-      xb = fmaxf(xb, __shfl_xor_sync(0xffffffffu, xb, 2));
-      if (__any_sync(0xffffffffu, xa > ma + kRescale || xb > mb + kRescale)) {
-        const float na = fmaxf(ma, xa), nb = fmaxf(mb, xb);
-        const float fa = ptx::ex2(ma - na), fb = ptx::ex2(mb - nb);
-        ma = na;
-        mb = nb;
-        la *= fa;
-        lb *= fb;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          o[i][0] *= fa;
-          o[i][1] *= fa;
-          o[i][2] *= fb;
-          o[i][3] *= fb;
-        }
-      }
-      // p in fp32 for the sum; rounded to bf16 for the product with V, the operand type of the
-      // matrix instruction (half a step, 2^-8, of each weight: the size of the output's own rounding)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        sc[i][0] = ptx::ex2(sc[i][0] - ma);
-        sc[i][1] = ptx::ex2(sc[i][1] - ma);
-        sc[i][2] = ptx::ex2(sc[i][2] - mb);
-        sc[i][3] = ptx::ex2(sc[i][3] - mb);
-        la += sc[i][0] + sc[i][1];
-        lb += sc[i][2] + sc[i][3];
-      }
-      const uint32_t pa[4] = {pack2(sc[0][0], sc[0][1]), pack2(sc[0][2], sc[0][3]), pack2(sc[1][0], sc[1][1]),
-                              pack2(sc[1][2], sc[1][3])};
-      // tokens past the end have p = 0, but their V may be anything: zero it
-      uint32_t k0 = 0xffffffffu, k1 = 0xffffffffu;
-      const bool cut = jw + 16 > j1;
-      if (cut) {
-        const int v = j1 - jw;
-        k0 = (cq < v ? 0xffffu : 0u) | (cq + 1 < v ? 0xffff0000u : 0u);
-        k1 = (cq + 8 < v ? 0xffffu : 0u) | (cq + 9 < v ? 0xffff0000u : 0u);
-      }
-#pragma unroll
-      for (int np = 0; np < 8; ++np) {
-        const int chunk = np * 2 + vcol;
-        uint32_t b[4];
-        ptx::ldsm4_t(vt + (chunk >> 3) * kHalf + vrow * 128 + (((chunk & 7) ^ (vrow & 7)) << 4), b);
+        const uint32_t pa[4] = {pack2(sc[0][0], sc[0][1]), pack2(sc[0][2], sc[0][3]), pack2(sc[1][0], sc[1][1]),
+                                pack2(sc[1][2], sc[1][3])};
+        // tokens past the end have p = 0, but their V may be anything: zero it
+        uint32_t k0 = 0xffffffffu, k1 = 0xffffffffu;
+        const bool cut = jw + 16 > q.kv;
         if (cut) {
-          b[0] &= k0;
-          b[1] &= k1;
-          b[2] &= k0;
-          b[3] &= k1;
+          const int v = q.kv - jw;
+          k0 = (cq < v ? 0xffffu : 0u) | (cq + 1 < v ? 0xffff0000u : 0u);
+          k1 = (cq + 8 < v ? 0xffffu : 0u) | (cq + 9 < v ? 0xffff0000u : 0u);
         }
-        ptx::mma16816(o[2 * np], pa, b[0], b[1]);
-        ptx::mma16816(o[2 * np + 1], pa, b[2], b[3]);
+#pragma unroll
+        for (int np = 0; np < 8; ++np) {
+          const int chunk = np * 2 + vcol;
+          uint32_t b[4];
+          ptx::ldsm4_t(vt + (chunk >> 3) * kHalf + vrow * 128 + (((chunk & 7) ^ (vrow & 7)) << 4), b);
+          if (cut) {
+            b[0] &= k0;
+            b[1] &= k1;
+            b[2] &= k0;
+            b[3] &= k1;
+          }
+          ptx::mma16816(o[2 * np], pa, b[0], b[1]);
+          ptx::mma16816(o[2 * np + 1], pa, b[2], b[3]);
+        }
       }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&empty[st]);
     }
-    __syncwarp();
-    if (lane == 0) ptx::mbar_arrive(&empty[st]);
+
+    // ------------------------------------------------------------ merge of the four warps
+    la += __shfl_xor_sync(0xffffffffu, la, 1);
+    lb += __shfl_xor_sync(0xffffffffu, lb, 1);
+    la += __shfl_xor_sync(0xffffffffu, la, 2);
+    lb += __shfl_xor_sync(0xffffffffu, lb, 2);
+    if ((lane & 3) == 0) {
+      ml[warp * 16 + ra] = make_float2(ma, la);
+      ml[warp * 16 + rb] = make_float2(mb, lb);
+    }
+    const bool whole = u.t0 == 0 && u.t1 == u.tiles;
+    // a part: this thread block's first slot if the unit began before its share, else its second
+    const long long slot = (2LL * cta + (u.t0 == 0 ? 1 : 0)) * kPagedRows;
+#pragma unroll
+    for (int rg = 0; rg < kPagedRows / kMergeRows; ++rg) {
+      if (rg * kMergeRows >= rows) break;
+      // lanes 16 (rg & 1) .. + 15 hold these rows, in their first or second half
+      if ((lane >> 4) == (rg & 1)) {
+        float* to = mo + (warp * kMergeRows + (ra & (kMergeRows - 1))) * kHeadDim + cq;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          *reinterpret_cast<float2*>(to + i * 8) = make_float2(o[i][rg & 2], o[i][(rg & 2) + 1]);
+      }
+      ptx::named_bar_sync(1, kWarps * 32);
+      const int r = rg * kMergeRows + warp, c = lane * 4;  // a warp per row
+      if (ok && r < rows) {
+        float m = kNoKey;
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) m = fmaxf(m, ml[i * 16 + r].x);
+        float l = 0.f;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < kWarps; ++i) {
+          const float2 e = ml[i * 16 + r];
+          const float f = ptx::ex2(e.x - m);
+          const float4 y = *reinterpret_cast<const float4*>(mo + (i * kMergeRows + warp) * kHeadDim + c);
+          l += e.y * f;
+          x.x += y.x * f;
+          x.y += y.y * f;
+          x.z += y.z * f;
+          x.w += y.w * f;
+        }
+        if (whole) {
+          const int tok = r / p.group;
+          const long long row = q.q0 + tok;
+          const int head = u.h * p.group + r - tok * p.group;
+          const float inv = l == 0.f ? 0.f : 1.0f / l;
+          *reinterpret_cast<uint2*>(p.out + row * p.out_stride + head * kHeadDim + c) =
+              make_uint2(pack2(x.x * inv, x.y * inv), pack2(x.z * inv, x.w * inv));
+          if (lane == 0) {
+            const float z = l > 0.f ? m + log2f(l) : l == 0.f ? -INFINITY : l;
+            const long long rh = row * p.q_heads + head;
+            if (p.lse != nullptr) p.lse[rh] = z * kLn2;
+            if (p.lse2 != nullptr) p.lse2[rh] = z;
+          }
+        } else {
+          *reinterpret_cast<float4*>(p.part + (slot + r) * kHeadDim + c) = x;
+          if (lane == 0) p.part_ml[slot + r] = make_float2(m, l);
+        }
+      }
+      ptx::named_bar_sync(1, kWarps * 32);
+    }
   }
   if (!ok && lane == 0) paged_report(w, kStatusTimeout);
-
-  // -------------------------------------------------------------- merge of the four warps
-  la += __shfl_xor_sync(0xffffffffu, la, 1);
-  lb += __shfl_xor_sync(0xffffffffu, lb, 1);
-  la += __shfl_xor_sync(0xffffffffu, la, 2);
-  lb += __shfl_xor_sync(0xffffffffu, lb, 2);
-  ptx::named_bar_sync(1, kWarps * 32);  // every tile was read: the stages' memory is free
-  float* mo = reinterpret_cast<float*>(smem);                                  // [warp][row][128]
-  float2* ml = reinterpret_cast<float2*>(smem + kWarps * 16 * kHeadDim * 4);  // [warp][row]
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    *reinterpret_cast<float2*>(mo + (warp * 16 + ra) * kHeadDim + i * 8 + cq) = make_float2(o[i][0], o[i][1]);
-    *reinterpret_cast<float2*>(mo + (warp * 16 + rb) * kHeadDim + i * 8 + cq) = make_float2(o[i][2], o[i][3]);
-  }
-  if ((lane & 3) == 0) {
-    ml[warp * 16 + ra] = make_float2(ma, la);
-    ml[warp * 16 + rb] = make_float2(mb, lb);
-  }
-  ptx::named_bar_sync(1, kWarps * 32);
-  if (!ok) return;
-  // one row at a time per warp, four columns per lane
-  for (int r = warp; r < rows; r += kWarps) {
-    float m = kNoKey;
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) m = fmaxf(m, ml[i * 16 + r].x);
-    float l = 0.f;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-      const float2 e = ml[i * 16 + r];
-      const float f = ptx::ex2(e.x - m);
-      const float4 y = *reinterpret_cast<const float4*>(mo + (i * 16 + r) * kHeadDim + lane * 4);
-      l += e.y * f;
-      x.x += y.x * f;
-      x.y += y.y * f;
-      x.z += y.z * f;
-      x.w += y.w * f;
-    }
-    const int tok = r / p.group;
-    const long long row = q.q0 + tok;
-    const int head = h * p.group + r - tok * p.group;
-    const long long rh = row * p.q_heads + head;
-    if (p.n_split > 1) {
-      const long long at = static_cast<long long>(sp) * w.n_rows * p.q_heads + rh;
-      *reinterpret_cast<float4*>(p.part + at * kHeadDim + lane * 4) = x;
-      if (lane == 0) p.part_ml[at] = make_float2(m, l);
-    } else {
-      const float inv = l > 0.f ? 1.0f / l : 0.f;
-      *reinterpret_cast<uint2*>(p.out + row * p.out_stride + head * kHeadDim + lane * 4) =
-          make_uint2(pack2(x.x * inv, x.y * inv), pack2(x.z * inv, x.w * inv));
-      if (lane == 0) {
-        const float z = l > 0.f ? m + log2f(l) : -INFINITY;
-        if (p.lse != nullptr) p.lse[rh] = z * kLn2;
-        if (p.lse2 != nullptr) p.lse2[rh] = z;
-      }
-    }
-  }
 }
 
-// ---------------------------------------------------------------- combine of parts
-// With parts i of a row, references m_i, sums l_i and unnormalised outputs o_i:
-//   m = max m_i, out = sum_i o_i 2^(m_i - m) / sum_i l_i 2^(m_i - m).
-// One block per (row, query head); its four warps take every fourth part.
-constexpr int kCombineThreads = 128;
+// ---------------------------------------------------------------- units that were cut
+// The unit that the start of share c cuts, if it is the first border inside that unit; its parts are the
+// second slot of thread block c - 1, then the first slots of c, c + 1, ... as far as the unit goes. With
+// references m_i, sums l_i and unnormalised outputs o_i of the parts:
+//   m = max m_i, out = sum_i o_i 2^(m_i - m) / sum_i l_i 2^(m_i - m), in the order of the parts.
+// A block takes 64 columns; sixteen lanes hold a row's, so a warp reads two parts at once, and the warps that
+// the unit's rows leave over (two per row for 8 rows, four for 4) take their share of the parts: all loads
+// leave together. (A warp per row, part after part: 13 us of 96 for 8 rows in 37 parts.)
+constexpr int kTokenJoinWarps = kPagedRows;
 
-__global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const __grid_constant__ PagedAttnParams p) {
-  __shared__ float factor[kPagedMaxSplit];
-  __shared__ float red[2][4];
-  __shared__ float4 acc[4][32];
-  const PagedView& w = p.view;
-  const int head = blockIdx.x % p.q_heads, row = blockIdx.x / p.q_heads;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+__global__ void __launch_bounds__(kTokenJoinWarps * 32)
+    paged_token_join_kernel(const __grid_constant__ PagedAttnParams p) {
+  __shared__ float4 sum[kTokenJoinWarps][16];
+  __shared__ float2 sum_ml[kTokenJoinWarps];
   ptx::let_next_launch();
-  const int s = paged_seq_of_row(w, row);
-  PagedSeq q = {};
-  if (s >= 0) q = paged_seq(w, s);
+  const int c = blockIdx.x / 2 + 1, col = (blockIdx.x & 1) * 64 + (threadIdx.x & 15) * 4;
   ptx::wait_previous();  // in every thread block, so that the kernel after this one may rely on it
-  if (s < 0 || !q.ok) return;
-  // keys that the row's block of tokens sees, and so the parts that were written
-  const int last_tok = min(q.n_q, ((row - q.q0) / p.block_tokens + 1) * p.block_tokens) - 1;
-  const int keys = p.causal ? max(0, q.kv - q.n_q + last_tok + 1) : q.kv;
-  const int n = (keys + p.split_keys - 1) / p.split_keys;
-  const long long rh = static_cast<long long>(row) * p.q_heads + head;
-  const long long step = static_cast<long long>(w.n_rows) * p.q_heads;
-  float m = kNoKey;
-  for (int i = threadIdx.x; i < n; i += kCombineThreads) m = fmaxf(m, p.part_ml[i * step + rh].x);
-  for (int d = 16; d; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-  if (lane == 0) red[0][warp] = m;
-  __syncthreads();
-  m = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
-  float l = 0.f;
-  for (int i = threadIdx.x; i < n; i += kCombineThreads) {
-    const float2 e = p.part_ml[i * step + rh];
-    const float f = ptx::ex2(e.x - m);
-    factor[i] = f;
-    l += e.y * f;
-  }
-  for (int d = 16; d; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-  if (lane == 0) red[1][warp] = l;
-  __syncthreads();
-  l = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
-  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+  const PagedCut cut = p.cuts[c];
+  const int rows = cut.n_q * p.group;
+  if (rows == 0) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int teams = kTokenJoinWarps / rows;
+  const int r = warp % rows, team = warp / rows;
+  float m = kNoKey, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](float2 e, float4 y) {
+    const float mn = fmaxf(m, e.x);
+    const float f = ptx::ex2(m - mn), f2 = ptx::ex2(e.x - mn);
+    m = mn;
+    l = l * f + e.y * f2;
+    o.x = o.x * f + y.x * f2;
+    o.y = o.y * f + y.y * f2;
+    o.z = o.z * f + y.z * f2;
+    o.w = o.w * f + y.w * f2;
+  };
+  if (team < teams) {
 #pragma unroll 4
-  for (int i = warp; i < n; i += 4) {
-    const float4 y = *reinterpret_cast<const float4*>(p.part + (i * step + rh) * kHeadDim + lane * 4);
-    const float f = factor[i];
-    x.x += y.x * f;
-    x.y += y.y * f;
-    x.z += y.z * f;
-    x.w += y.w * f;
+    for (int i = team * 2 + (lane >> 4); i < cut.parts; i += teams * 2) {
+      const long long at = (i == 0 ? 2LL * c - 1 : 2LL * (c - 1 + i)) * kPagedRows + r;
+      add(p.part_ml[at], *reinterpret_cast<const float4*>(p.part + at * kHeadDim + col));
+    }
   }
-  acc[warp][lane] = x;
+  float2 e;
+  float4 y;
+  e.x = __shfl_down_sync(0xffffffffu, m, 16);
+  e.y = __shfl_down_sync(0xffffffffu, l, 16);
+  y.x = __shfl_down_sync(0xffffffffu, o.x, 16);
+  y.y = __shfl_down_sync(0xffffffffu, o.y, 16);
+  y.z = __shfl_down_sync(0xffffffffu, o.z, 16);
+  y.w = __shfl_down_sync(0xffffffffu, o.w, 16);
+  add(e, y);
+  if (lane < 16) sum[warp][lane] = o;
+  if (lane == 0) sum_ml[warp] = make_float2(m, l);
   __syncthreads();
-  if (warp != 0) return;
-  float4 y = acc[0][lane];
-  for (int i = 1; i < 4; ++i) {
-    y.x += acc[i][lane].x;
-    y.y += acc[i][lane].y;
-    y.z += acc[i][lane].z;
-    y.w += acc[i][lane].w;
-  }
-  const float inv = l > 0.f ? 1.0f / l : 0.f;
-  *reinterpret_cast<uint2*>(p.out + row * p.out_stride + head * kHeadDim + lane * 4) =
-      make_uint2(pack2(y.x * inv, y.y * inv), pack2(y.z * inv, y.w * inv));
-  if (lane == 0) {
-    const float z = l > 0.f ? m + log2f(l) : -INFINITY;
+  if (team != 0 || lane >= 16) return;
+  for (int i = 1; i < teams; ++i) add(sum_ml[i * rows + r], sum[i * rows + r][lane]);
+  const int tok = r / p.group;
+  const long long row = cut.row0 + tok;
+  const int head = cut.h * p.group + r - tok * p.group;
+  const float inv = l == 0.f ? 0.f : 1.0f / l;
+  *reinterpret_cast<uint2*>(p.out + row * p.out_stride + head * kHeadDim + col) =
+      make_uint2(pack2(o.x * inv, o.y * inv), pack2(o.z * inv, o.w * inv));
+  if (col == 0) {
+    const float z = l > 0.f ? m + log2f(l) : l == 0.f ? -INFINITY : l;
+    const long long rh = row * p.q_heads + head;
     if (p.lse != nullptr) p.lse[rh] = z * kLn2;
     if (p.lse2 != nullptr) p.lse2[rh] = z;
   }
@@ -386,35 +517,55 @@ __global__ void __launch_bounds__(kCombineThreads) paged_combine_kernel(const __
 
 // ---------------------------------------------------------------- attention weight of single tokens
 // The scores that the attention kept (masked ones -infinity) and the rows' log-sum-exp: a key gathers
-// the sum over the stream's at most 16 rows of 2^(score - z). One thread per key. Keeping a score costs 8
+// the sum over the stream's at most 16 rows of 2^(score - z). Keeping a score costs 8
 // bytes of traffic per row and key; reading K again would cost 256 for all rows.
 constexpr int kTokenWeightThreads = 256;
+constexpr int kTokenWeightKeys = 4;  // per thread
+constexpr int kTokenWeightTile = kTokenWeightThreads * kTokenWeightKeys;
 
 __global__ void __launch_bounds__(kTokenWeightThreads)
     paged_token_weight_kernel(const __grid_constant__ PagedAttnParams p) {
   const PagedView& w = p.view;
-  const int n_kt = (w.max_kv + kTokenWeightThreads - 1) / kTokenWeightThreads;
+  const int n_kt = (w.max_kv + kTokenWeightTile - 1) / kTokenWeightTile;
   const int sh = blockIdx.x / n_kt;
   const int h = sh % w.kv_heads, s = sh / w.kv_heads;
-  const int j = (blockIdx.x - sh * n_kt) * kTokenWeightThreads + threadIdx.x;
+  const int j0 = (blockIdx.x - sh * n_kt) * kTokenWeightTile + threadIdx.x;
   const PagedSeq q = paged_seq(w, s);
+  float* to = p.weight + (static_cast<long long>(s) * w.kv_heads + h) * p.weight_stride;
+  const int fresh = q.kv - q.n_q;  // the chunk's own keys start from zero
   ptx::wait_previous();
-  if (!q.ok || q.n_q == 0 || j >= q.kv) return;
-  float sum = 0.f;
+  if (!q.ok || q.n_q == 0 || j0 >= q.kv) return;
+  float old[kTokenWeightKeys], sum[kTokenWeightKeys];
+#pragma unroll
+  for (int k = 0; k < kTokenWeightKeys; ++k) {
+    const int j = j0 + k * kTokenWeightThreads;
+    old[k] = j < fresh ? to[j] : 0.f;
+    sum[k] = 0.f;
+  }
   for (int t = 0; t < q.n_q; ++t) {
     const long long rh = static_cast<long long>(q.q0 + t) * p.q_heads + h * p.group;
 #pragma unroll 4
-    for (int g = 0; g < p.group; ++g)
-      sum += ptx::ex2(p.scores[(rh + g) * p.score_stride + j] - p.lse2[rh + g]);
+    for (int g = 0; g < p.group; ++g) {
+      const float z = p.lse2[rh + g];
+      const float* sc = p.scores + (rh + g) * p.score_stride;
+#pragma unroll
+      for (int k = 0; k < kTokenWeightKeys; ++k) {
+        const int j = j0 + k * kTokenWeightThreads;
+        if (j < q.kv) sum[k] += ptx::ex2(sc[j] - z);
+      }
+    }
   }
-  float* to = p.weight + (static_cast<long long>(s) * w.kv_heads + h) * p.weight_stride + j;
-  *to = (j < q.kv - q.n_q ? *to : 0.f) + sum;
+#pragma unroll
+  for (int k = 0; k < kTokenWeightKeys; ++k) {
+    const int j = j0 + k * kTokenWeightThreads;
+    if (j < q.kv) to[j] = old[k] + sum[k];
+  }
 }
 
 }  // namespace
 
 cudaError_t launch_paged_token_weight(const PagedAttnParams& p, cudaStream_t stream) {
-  const unsigned n_kt = (p.view.max_kv + kTokenWeightThreads - 1) / kTokenWeightThreads;
+  const unsigned n_kt = (p.view.max_kv + kTokenWeightTile - 1) / kTokenWeightTile;
   return launch_after(paged_token_weight_kernel, n_kt * p.view.n_seqs * p.view.kv_heads, kTokenWeightThreads, 0, stream, p);
 }
 
@@ -436,13 +587,10 @@ cudaError_t launch_paged_decode(const CUtensorMap& tm_k, const CUtensorMap& tm_v
       configured[dev] = true;
     }
   }
-  const unsigned grid = static_cast<unsigned>(p.view.n_seqs) * p.view.kv_heads * p.n_split;
-  paged_decode_kernel<<<grid, kDecodeThreads, kDecodeSmem, stream>>>(tm_k, tm_v, p);
-  return cudaGetLastError();
-}
-
-cudaError_t launch_paged_combine(const PagedAttnParams& p, cudaStream_t stream) {
-  return launch_after(paged_combine_kernel, static_cast<unsigned>(p.view.n_rows) * p.q_heads, kCombineThreads, 0, stream, p);
+  paged_decode_kernel<<<2 * kSmCount, kDecodeThreads, kDecodeSmem, stream>>>(tm_k, tm_v, p);
+  err = cudaGetLastError();
+  if (err != cudaSuccess) return err;
+  return launch_after(paged_token_join_kernel, 2 * (2 * kSmCount - 1), kTokenJoinWarps * 32, 0, stream, p);
 }
 
 }  // namespace rkv

@@ -85,31 +85,15 @@ int check_heads(const rkv_page_pool* pool, int q_heads, int n_rows) {
   return RKV_OK;
 }
 
-// How the call is cut up.
-// Single-token form: a thread block takes one (stream, KV head), two to an SM; a key stream is split so that
-// the batch, were every stream max_kv long, would give each SM's two places four blocks (shorter
-// streams then give fewer, never idle ones), but no shorter than kMinSplit tokens, below which a
-// block's fixed cost outweighs its share.
-// Chunk form: one thread block per SM; they share the batch's key tiles evenly, whatever the lengths
-// (paged_plan_kernel).
-constexpr int kMinSplit = 256;
-
+// Which form a call takes, and its workspace. The single-token form serves up to 16 rows per stream and KV
+// head, which fill one warp-level matrix instruction; above that the chunk form's tiles of 128 rows
+// are the better use (17 rows: both are bound by HBM).
 rkv::PagedPlan plan_of(const rkv_page_pool* pool, const rkv_paged_batch* b, int q_heads, int n_rows, bool weight) {
   rkv::PagedPlan p;
   std::memset(&p, 0, sizeof(p));
   const int group = q_heads / pool->kv_heads;
   p.rows_form = static_cast<long long>(b->max_q) * group <= rkv::kPagedRows;
-  if (p.rows_form) {
-    p.block_tokens = b->max_q > 0 ? b->max_q : 1;
-    p.n_blocks = b->n_seqs;
-    const long long blocks = static_cast<long long>(b->n_seqs) * pool->kv_heads;
-    const long long want = 8LL * rkv::kSmCount;
-    long long len = std::max<long long>((b->max_kv * blocks + want - 1) / want, kMinSplit);
-    len = std::max<long long>(len, (b->max_kv + rkv::kPagedMaxSplit - 1) / rkv::kPagedMaxSplit);
-    len = (len + rkv::kPagedDecodeTile - 1) / rkv::kPagedDecodeTile * rkv::kPagedDecodeTile;
-    p.split_keys = static_cast<int>(len);
-    p.n_split = std::max(1, static_cast<int>((b->max_kv + len - 1) / len));
-  } else {
+  if (!p.rows_form) {
     p.block_tokens = 2 * (rkv::kQueryBox / group);
     const long long per_seq = (static_cast<long long>(b->max_q) + p.block_tokens - 1) / p.block_tokens;
     p.n_blocks = static_cast<int>(std::min(static_cast<long long>(n_rows) / p.block_tokens + b->n_seqs,
@@ -127,14 +111,13 @@ rkv::PagedPlan plan_of(const rkv_page_pool* pool, const rkv_paged_batch* b, int 
     return at;
   };
   p.lse = weight ? take(4 * heads) : -1;
-  p.part = p.part_ml = p.blocks = p.work = p.seq_first = -1;
-  if (p.rows_form && p.n_split > 1) {
-    p.part = take(4 * heads * kHeadDim * p.n_split);
-    p.part_ml = take(8 * heads * p.n_split);
-  } else if (!p.rows_form) {
-    const long long rows = 2LL * rkv::kSmCount * rkv::kPagedPartRows;
-    p.part = take(4 * rows * kHeadDim);
-    p.part_ml = take(8 * rows);
+  p.cuts = p.blocks = p.work = p.seq_first = -1;
+  const long long rows = p.rows_form ? 4LL * rkv::kSmCount * rkv::kPagedRows : 2LL * rkv::kSmCount * rkv::kPagedPartRows;
+  p.part = take(4 * rows * kHeadDim);
+  p.part_ml = take(8 * rows);
+  if (p.rows_form) {
+    p.cuts = take(2LL * rkv::kSmCount * sizeof(rkv::PagedCut));
+  } else {
     p.blocks = take(static_cast<long long>(sizeof(rkv::PagedBlock)) * p.n_blocks);
     p.work = take(sizeof(rkv::PagedWork));
     p.seq_first = take(4LL * b->n_seqs);
@@ -228,6 +211,7 @@ RKV_API int rkv_paged_attention(const rkv_page_pool* pool, const rkv_paged_batch
   if (plan.lse >= 0) p.lse2 = reinterpret_cast<float*>(ws + plan.lse);
   if (plan.part >= 0) p.part = reinterpret_cast<float*>(ws + plan.part);
   if (plan.part_ml >= 0) p.part_ml = reinterpret_cast<float2*>(ws + plan.part_ml);
+  if (plan.cuts >= 0) p.cuts = reinterpret_cast<rkv::PagedCut*>(ws + plan.cuts);
   if (plan.blocks >= 0) {
     p.blocks = reinterpret_cast<rkv::PagedBlock*>(ws + plan.blocks);
     p.work = reinterpret_cast<rkv::PagedWork*>(ws + plan.work);
@@ -237,8 +221,6 @@ RKV_API int rkv_paged_attention(const rkv_page_pool* pool, const rkv_paged_batch
   p.score_stride = plan.score_stride;
   p.block_tokens = plan.block_tokens;
   p.n_blocks = plan.n_blocks;
-  p.split_keys = plan.split_keys;
-  p.n_split = plan.n_split;
   p.wait_limit_ns = kWaitNs;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t err;
@@ -247,7 +229,6 @@ RKV_API int rkv_paged_attention(const rkv_page_pool* pool, const rkv_paged_batch
   if (!encode_pages(&tm_k, pool->k, pool, tile) || !encode_pages(&tm_v, pool->v, pool, tile)) return RKV_ERR_CUDA;
   if (plan.rows_form) {
     err = rkv::launch_paged_decode(tm_k, tm_v, p, st);
-    if (err == cudaSuccess && plan.n_split > 1) err = rkv::launch_paged_combine(p, st);
     if (err == cudaSuccess && weight != nullptr && batch->max_kv > 0) err = rkv::launch_paged_token_weight(p, st);
   } else {
     if (!rkv::encode_map(&tm_q, q, q_heads, n_rows, kHeadDim * 2, static_cast<uint64_t>(q_stride) * 2, p.group,
