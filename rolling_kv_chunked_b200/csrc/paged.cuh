@@ -8,16 +8,16 @@
 
 namespace rkv {
 
-// Launch a kernel of a call's chain that may be set up while the one before it still runs; it
-// waits for that one's results itself (ptx::wait_previous, in every thread block).
+// Launch a kernel that may be set up while the stream's previous one still runs; it waits for that one
+// itself (ptx::wait_previous, in every thread block, before it touches memory).
 template <typename... P, typename... A>
-cudaError_t launch_after(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t stream,
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, unsigned block, size_t smem, cudaStream_t stream,
                          A&&... args) {
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(block);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;

@@ -148,14 +148,14 @@ struct PagedWriteParams {
 
 // How a call is cut up (a host rule on the batch's host values; workspace offsets in bytes).
 struct PagedPlan {
-  int rows_form;     // 1: at most kPagedRows rows per stream and KV head, the form for single tokens
+  int slot_rows;     // single-token form: rows of a stream and KV head, rounded up to 16 or 32; 0: chunk form
   int block_tokens;  // chunk form: tokens of one unit of rows
   int n_blocks;      // and such units of one KV head in the batch at most
   long long lse, part, part_ml, scores, cuts, blocks, work, seq_first, total;  // -1: not used
   long long score_stride;
 };
 
-constexpr int kPagedRows = 16;
+constexpr int kPagedRows = 32;  // rows of the single-token form at most
 
 // Work of the chunk form, laid out on the device by a small kernel from the lengths of the moment
 // (workspace). A block of up to block_tokens chunk tokens of one stream, for every KV head the same:
@@ -172,13 +172,24 @@ struct PagedBlock {
 // heads' tiles W. In step (units of nearly one size): every thread block takes `waves` whole units; of the
 // last n_tail, thread block i < n_tail takes the first `quota` tiles of unit i, and the others share
 // what is left of them, `quota` tiles each, in a row.
+struct PagedShare {  // one thread block's
+  long long left;  // tiles (in step: of the last units)
+  int h, b, t;     // in a row: head, block and tile of its first
+  int i, pos;      // in step, sharing leftovers: the last unit it begins in, and its first leftover tile
+  int unused;
+};
+struct PagedJoin {  // a unit that was shared: parts in slots slot0, slot0 + 1, slot0 + 1 + step, ... (parts 0: none)
+  int b, h, slot0, step, parts;
+  int unused[3];
+};
 struct PagedWork {
   int n_blocks;
-  int head_tiles;  // key tiles of all blocks (one KV head)
   int n_ctas;
   int in_step;
   int waves, n_tail, quota;
-  int rest[kSmCount + 1];  // in step: tiles left of the last units before unit i
+  int rest[kSmCount + 2];  // in step: tiles left of the last units before unit i
+  PagedShare share[kSmCount];
+  PagedJoin join[kSmCount];
 };
 // Single-token form: the unit that the start of a share cuts (n_q 0: none, or an earlier border cuts it).
 struct PagedCut {
@@ -197,7 +208,7 @@ struct PagedAttnParams {
   float scale_log2;  // log2(e) / sqrt(d)
   // workspace
   float* lse2;      // [n_rows][q_heads], log2; null when no weight is wanted
-  float* part;      // unnormalised sums of p v of cut units: [4 * kSmCount][kPagedRows][128] (single-token
+  float* part;      // unnormalised sums of p v of cut units: [4 * kSmCount][slot_rows][128] (single-token
                     // form) or [2 * kSmCount][kPagedPartRows][128]
   float2* part_ml;  // the same rows: reference (log2) and sum of p
   PagedCut* cuts;      // single-token form: [2 * kSmCount]
@@ -206,7 +217,8 @@ struct PagedAttnParams {
   int* seq_first;      // chunk form: [n_seqs], the stream's first block
   float* scores;    // [n_rows][q_heads][score_stride]: log2 scores of the single-token form; null: not kept
   long long score_stride;
-  int block_tokens, n_blocks;
+  int slot_rows;                // single-token form
+  int block_tokens, n_blocks;  // chunk form
   unsigned long long wait_limit_ns;
 };
 

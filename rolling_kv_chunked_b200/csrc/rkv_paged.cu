@@ -15,6 +15,8 @@ constexpr int kWriteWarps = 4;
 
 __global__ void __launch_bounds__(kWriteWarps * 32) paged_write_kernel(const __grid_constant__ PagedWriteParams p) {
   const PagedView& w = p.view;
+  ptx::let_next_launch();
+  ptx::wait_previous();
   const int row = blockIdx.x * kWriteWarps + (threadIdx.x >> 5);
   if (row >= w.n_rows) return;
   const int s = paged_seq_of_row(w, row);
@@ -85,6 +87,7 @@ __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(const __grid_
   const int rank = blockIdx.x % size, sh = blockIdx.x / size;
   const int s = sh / w.kv_heads;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  ptx::wait_previous();
   const int n = __ldg(w.kv_len + s);
   int* kept = p.kept + static_cast<long long>(sh) * p.keep;
   const bool bad = n < 0 || n > w.max_kv;
@@ -414,8 +417,7 @@ cudaError_t configure() {
 
 cudaError_t launch_paged_write(const PagedWriteParams& p, cudaStream_t stream) {
   const int grid = (p.view.n_rows + kWriteWarps - 1) / kWriteWarps;
-  paged_write_kernel<<<grid, kWriteWarps * 32, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_after(paged_write_kernel, grid, kWriteWarps * 32, 0, stream, p);
 }
 
 cudaError_t launch_paged_evict(const PagedEvictParams& p, cudaStream_t stream) {
@@ -433,14 +435,14 @@ cudaError_t launch_paged_evict(const PagedEvictParams& p, cudaStream_t stream) {
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = size;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // for the second kernel
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(heads * size);
   cfg.blockDim = dim3(kSelThreads);
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   err = held ? cudaLaunchKernelEx(&cfg, paged_select_kernel<true>, p)
              : cudaLaunchKernelEx(&cfg, paged_select_kernel<false>, p);
   if (err != cudaSuccess) return err;
@@ -448,7 +450,6 @@ cudaError_t launch_paged_evict(const PagedEvictParams& p, cudaStream_t stream) {
   size = kMoveCluster;
   while (size > 1 && heads * 2 * kMoveParts * size > 1024) size /= 2;
   attr[0].val.clusterDim.x = size;
-  cfg.numAttrs = 2;
   cfg.gridDim = dim3(heads * (2 * kMoveParts + 1) * size);
   cfg.blockDim = dim3(kMoveThreads);
   cfg.dynamicSmemBytes = kMoveSmem;

@@ -92,10 +92,27 @@ __device__ __forceinline__ int plan_scan(int x, int* warp_sums, int& total) {
   return inc - x + __reduce_add_sync(0xffffffffu, lane < wp ? v : 0);
 }
 
-// One thread block: the units of the batch and their key tiles, from the lengths on the device.
+// The last of n rising values that is at most y: in shared memory if they fit there, else in `far`.
+__device__ __forceinline__ int last_at_most(const int* near, const int* far, int stride, int n, int y) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int m = (lo + hi) >> 1;
+    const int v = n <= kPlanThreads ? near[m] : far[static_cast<long long>(m) * stride];
+    if (v <= y) lo = m; else hi = m;
+  }
+  return lo;
+}
+
+// One thread block: the units of the batch and their key tiles, from the lengths on the device, and how
+// they are shared.
 __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_constant__ PagedAttnParams p) {
   __shared__ int warp_sums[32];
+  __shared__ int sizes[2][32];
+  __shared__ int near_seq[kPlanThreads];        // first block of every stream, if there are that few
+  __shared__ int near_start[kPlanThreads + 1];  // first tile of every block
+  __shared__ int near_rest[kSmCount + 2];
   ptx::let_next_launch();
+  ptx::wait_previous();
   const PagedView& w = p.view;
   const int t = threadIdx.x;
   int blocks = 0;
@@ -112,6 +129,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
     int total;
     const int first = blocks + plan_scan(c, warp_sums, total);
     if (s < w.n_seqs) p.seq_first[s] = first;
+    if (base == 0) near_seq[t] = first;
     blocks += total;
   }
   __syncthreads();
@@ -125,18 +143,14 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
     const int b = base + t;
     PagedBlock k = {};
     if (b < blocks) {
-      int lo = 0, hi = w.n_seqs;  // the last stream whose first block is at or before b
-      while (hi - lo > 1) {
-        const int m = (lo + hi) >> 1;
-        if (p.seq_first[m] <= b) lo = m; else hi = m;
-      }
-      const PagedSeq q = paged_seq(w, lo);
-      const int i0 = (b - p.seq_first[lo]) * p.block_tokens;
+      const int s = last_at_most(near_seq, p.seq_first, 1, w.n_seqs, b);
+      const PagedSeq q = paged_seq(w, s);
+      const int i0 = (b - (w.n_seqs <= kPlanThreads ? near_seq[s] : p.seq_first[s])) * p.block_tokens;
       k.row0 = q.q0 + i0;
       k.cnt = min(p.block_tokens, q.n_q - i0);
       k.keys = p.causal ? max(0, q.kv - q.n_q + i0 + k.cnt) : q.kv;
       k.place0 = q.kv - q.n_q + i0;
-      k.seq = lo;
+      k.seq = s;
       k.tiles = max(1, (k.keys + kBN - 1) / kBN);
       most = max(most, k.tiles);
       least = min(least, k.tiles);
@@ -144,27 +158,34 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
     int total;
     k.start = tiles + plan_scan(k.tiles, warp_sums, total);
     if (b < blocks) p.blocks[b] = k;
+    if (base == 0) {
+      near_start[t] = k.start;
+      if (t == kPlanThreads - 1) near_start[kPlanThreads] = k.start + k.tiles;
+    }
     tiles += total;
   }
-  // the whole block's largest and smallest
+  // the whole thread block's largest and smallest
   most = __reduce_max_sync(0xffffffffu, most);
   least = __reduce_min_sync(0xffffffffu, least);
+  if ((t & 31) == 0) {
+    sizes[0][t >> 5] = most;
+    sizes[1][t >> 5] = least;
+  }
   __syncthreads();
-  if ((t & 31) == 0) warp_sums[t >> 5] = most;
-  __syncthreads();
-  most = __reduce_max_sync(0xffffffffu, warp_sums[t & 31]);
-  __syncthreads();
-  if ((t & 31) == 0) warp_sums[t >> 5] = least;
-  __syncthreads();
-  least = __reduce_min_sync(0xffffffffu, warp_sums[t & 31]);
+  most = __reduce_max_sync(0xffffffffu, sizes[0][t & 31]);
+  least = __reduce_min_sync(0xffffffffu, sizes[1][t & 31]);
+  auto tiles_of = [&](int b) {
+    return blocks <= kPlanThreads ? (b + 1 < blocks ? near_start[b + 1] : tiles) - near_start[b] : p.blocks[b].tiles;
+  };
+  auto start_of = [&](int b) { return blocks <= kPlanThreads ? near_start[b] : p.blocks[b].start; };
 
   const long long units = static_cast<long long>(blocks) * w.kv_heads;
   const long long all = static_cast<long long>(tiles) * w.kv_heads;
   PagedWork* out = p.work;
-  const int waves = static_cast<int>(units / kSmCount), n_tail = static_cast<int>(units % kSmCount);
+  const int waves = static_cast<int>(units / kSmCount), n_tail = static_cast<int>(units - static_cast<long long>(waves) * kSmCount);
   const long long first = static_cast<long long>(waves) * kSmCount;  // the first of the last units
   int n = 0;  // thread i < n_tail: tiles of the i-th of them
-  if (t < n_tail) n = p.blocks[(first + t) % blocks].tiles;
+  if (t < n_tail) n = tiles_of(static_cast<int>((first + t) % blocks));
   int tail_tiles;
   plan_scan(n, warp_sums, tail_tiles);
   const int quota = (tail_tiles + kSmCount - 1) / kSmCount;
@@ -172,38 +193,64 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
   const bool in_step = blocks > 0 && least >= most - most / 8 && (n_tail == 0 || quota >= kMinTiles);
   int rest_tiles;
   const int rest = plan_scan(max(0, n - quota), warp_sums, rest_tiles);
-  if (t <= n_tail) out->rest[t] = rest;
+  if (t <= n_tail) out->rest[t] = near_rest[t] = rest;
+  const int n_ctas = in_step ? kSmCount
+                             : static_cast<int>(min(static_cast<long long>(kSmCount), (all + kMinTiles - 1) / kMinTiles));
   if (t == 0) {
     out->n_blocks = blocks;
-    out->head_tiles = tiles;
+    out->n_ctas = n_ctas;
     out->in_step = in_step;
     out->waves = waves;
     out->n_tail = n_tail;
     out->quota = quota;
-    out->n_ctas = in_step ? kSmCount
-                          : static_cast<int>(min(static_cast<long long>(kSmCount), (all + kMinTiles - 1) / kMinTiles));
   }
-}
-
-// First tile of thread block c's share, counted over all heads.
-__device__ __forceinline__ long long share_start(const PagedWork& r, int kv_heads, int c) {
-  return static_cast<long long>(r.head_tiles) * kv_heads * c / r.n_ctas;
-}
-
-// The block of chunk tokens that holds tile y of a head. A whole warp calls it; 32 blocks are probed at
-// a time.
-__device__ __forceinline__ int find_block(const PagedBlock* blocks, int n, int y) {
-  const int lane = threadIdx.x & 31;
-  int lo = 0, hi = n;  // the answer is the last block whose start is <= y: in [lo, hi)
-  while (hi - lo > 1) {
-    const int step = (hi - lo + 31) / 32;
-    const int i = lo + lane * step;
-    const bool le = i < hi && blocks[i].start <= y;
-    const int c = max(1, __popc(__ballot_sync(0xffffffffu, le)));
-    hi = min(hi, lo + c * step);
-    lo += (c - 1) * step;
+  __syncthreads();
+  if (t >= kSmCount) return;
+  PagedShare mine = {};
+  PagedJoin join = {};
+  if (in_step) {
+    const int helpers = kSmCount - n_tail;
+    if (t < n_tail) {
+      mine.left = quota;
+      const int r0 = near_rest[t], r1 = near_rest[t + 1];
+      if (r1 > r0) {
+        const int j0 = min(helpers - 1, r0 / quota), j1 = min(helpers - 1, (r1 - 1) / quota);
+        join.h = static_cast<int>((first + t) / blocks);
+        join.b = static_cast<int>(first + t - static_cast<long long>(join.h) * blocks);
+        join.slot0 = 2 * t + j0;
+        join.step = 1;
+        join.parts = j1 - j0 + 2;
+      }
+    } else {
+      mine.pos = min(rest_tiles, (t - n_tail) * quota);
+      mine.left = (t == kSmCount - 1 ? rest_tiles : min(rest_tiles, mine.pos + quota)) - mine.pos;
+      int hi = n_tail;  // the last unit whose leftover begins at or before pos
+      while (hi - mine.i > 1) {
+        const int m = (mine.i + hi) >> 1;
+        if (near_rest[m] <= mine.pos) mine.i = m; else hi = m;
+      }
+    }
+  } else if (t < n_ctas) {
+    auto border = [&](int c) { return all * c / n_ctas; };
+    const long long x = border(t);
+    mine.left = border(t + 1) - x;
+    mine.h = static_cast<int>(x / tiles);
+    const int y = static_cast<int>(x - static_cast<long long>(mine.h) * tiles);
+    mine.b = last_at_most(near_start, &p.blocks[0].start, sizeof(PagedBlock) / 4, blocks, y);
+    mine.t = y - start_of(mine.b);
+    // the unit that this share's start cuts, if it is the first border inside it
+    const long long begin = x - mine.t, end = begin + tiles_of(mine.b);
+    if (mine.t > 0 && border(t - 1) <= begin) {
+      join.b = mine.b;
+      join.h = mine.h;
+      join.slot0 = 2 * t - 1;
+      join.step = 2;
+      join.parts = 2;
+      while (t + join.parts - 1 < n_ctas && border(t + join.parts - 1) < end) ++join.parts;
+    }
   }
-  return lo;
+  out->share[t] = mine;
+  out->join[t] = join;
 }
 
 // In step: the thread block (of those past n_tail, counted from 0) that takes leftover tile y.
@@ -429,7 +476,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   float4* chain = reinterpret_cast<float4*>(smem + kSmemChain);  // [2][128]: reference, sum, pending factor
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kSmemBar);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kNumBars);
-  int* found = reinterpret_cast<int*>(bars + kNumBars + 1);
   const PagedView& w = p.view;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const unsigned long long limit = p.wait_limit_ns;
@@ -448,34 +494,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   walk.tpt = tpt;
   walk.cta = cta;
   walk.in_step = work.in_step != 0;
-  walk.wave = walk.i = walk.pos = 0;
-  int y0 = 0;
-  if (!walk.in_step) {
-    const long long x0 = share_start(work, w.kv_heads, cta);
-    walk.left = share_start(work, w.kv_heads, cta + 1) - x0;
-    walk.h = static_cast<int>(x0 / work.head_tiles);
-    y0 = static_cast<int>(x0 - static_cast<long long>(walk.h) * work.head_tiles);
-  } else if (cta < work.n_tail) {
-    walk.left = work.quota;
-  } else {
-    const int all = work.rest[work.n_tail];
-    walk.pos = min(all, (cta - work.n_tail) * work.quota);
-    walk.left = (cta == kSmCount - 1 ? all : min(all, walk.pos + work.quota)) - walk.pos;
-    int hi = work.n_tail;  // the last unit whose leftover begins at or before pos
-    while (hi - walk.i > 1) {
-      const int m = (walk.i + hi) >> 1;
-      if (work.rest[m] <= walk.pos) walk.i = m; else hi = m;
-    }
-  }
-  if (warp == 0) {
-    if (!walk.in_step) {
-      const int b = find_block(p.blocks, work.n_blocks, y0);
-      if (lane == 0) {
-        found[0] = b;
-        found[1] = p.blocks[b].start;
-      }
-    }
-  } else if (threadIdx.x == 32) {
+  walk.wave = 0;
+  const PagedShare& share = work.share[cta];
+  walk.left = share.left;
+  walk.h = share.h;
+  walk.b = share.b;
+  walk.t = share.t;
+  walk.i = share.i;
+  walk.pos = share.pos;
+  if (threadIdx.x == 32) {
     ptx::mbar_init(&bars[kBarQ], 1);
     ptx::mbar_init(&bars[kBarQEmpty], 1);
     for (int i = 0; i < 2; ++i) {
@@ -505,10 +532,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  if (!walk.in_step) {
-    walk.b = found[0];
-    walk.t = y0 - found[1];
-  }
   PagedUnit u;
 
   if (warp == 8) {
@@ -785,55 +808,27 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------- units that were shared
-// Work shared in a row: the unit that the start of share c cuts, if it is the first border inside that
-// unit; its parts are the second slot of thread block c - 1, then the first slots of c, c + 1, ... as far
-// as the unit goes. In step: the c-th of the last units; its first part, then the helpers', in
-// consecutive slots. One warp per row, in the order of the parts.
+// Their parts are added up in order, one warp per row. (Shared in a row: the second slot of the thread block that
+// began the unit, then the first slots of those after it; in step: the first part's, then the helpers'.)
 constexpr int kJoinThreads = 256;
 constexpr int kJoinSlices = kPagedPartRows / (kJoinThreads / 32);  // a row per warp
 
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ PagedAttnParams p) {
   ptx::let_next_launch();
   ptx::wait_previous();
-  const PagedView& w = p.view;
-  const int c = blockIdx.x / kJoinSlices, slice = blockIdx.x % kJoinSlices;
-  const PagedWork& work = *p.work;
-  int h, b, slot0, step, parts;
-  if (work.in_step) {
-    if (c >= work.n_tail) return;
-    const int left = work.rest[c + 1] - work.rest[c];
-    if (left == 0) return;
-    const int j0 = helper_of(work, work.rest[c]), j1 = helper_of(work, work.rest[c + 1] - 1);
-    const long long n = static_cast<long long>(work.waves) * kSmCount + c;
-    h = static_cast<int>(n / work.n_blocks);
-    b = static_cast<int>(n - static_cast<long long>(h) * work.n_blocks);
-    slot0 = 2 * c + j0;
-    step = 1;
-    parts = j1 - j0 + 2;
-  } else {
-    if (c == 0 || c >= work.n_ctas) return;
-    const long long x = share_start(work, w.kv_heads, c);
-    h = static_cast<int>(x / work.head_tiles);
-    const long long head0 = static_cast<long long>(h) * work.head_tiles;
-    b = find_block(p.blocks, work.n_blocks, static_cast<int>(x - head0));
-    const long long first = head0 + p.blocks[b].start, end = first + p.blocks[b].tiles;
-    if (x == first || share_start(work, w.kv_heads, c - 1) > first) return;  // no cut, or not the first
-    parts = 2;
-    while (c + parts - 1 < work.n_ctas && share_start(work, w.kv_heads, c + parts - 1) < end) ++parts;
-    slot0 = 2 * c - 1;
-    step = 2;
-  }
-  const PagedBlock k = p.blocks[b];
+  const PagedJoin join = p.work->join[blockIdx.x / kJoinSlices];
+  if (join.parts == 0) return;
+  const PagedBlock k = p.blocks[join.b];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tpt = kBM / p.group;
-  const int rr = slice * (kJoinThreads / 32) + warp;  // row of the unit
+  const int rr = blockIdx.x % kJoinSlices * (kJoinThreads / 32) + warp;  // row of the unit
   const int tile = rr / kBM, r = rr % kBM, tok = r / p.group;
   if (r >= tpt * p.group || tile * tpt + tok >= k.cnt) return;
   float m = kNoKey, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (int i = 0; i < parts; ++i) {
-    const long long at = static_cast<long long>(i == 0 ? slot0 : slot0 + 1 + (i - 1) * step) * kPagedPartRows + rr;
+  for (int i = 0; i < join.parts; ++i) {
+    const long long at = static_cast<long long>(i == 0 ? join.slot0 : join.slot0 + 1 + (i - 1) * join.step) * kPagedPartRows + rr;
     const float2 e = p.part_ml[at];
     const float4 y = *reinterpret_cast<const float4*>(p.part + at * kHeadDim + lane * 4);
     const float mn = fmaxf(m, e.x);
@@ -846,7 +841,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
     o.w = o.w * f + y.w * f2;
   }
   const long long row = k.row0 + tile * tpt + tok;
-  const int head = h * p.group + r - tok * p.group;
+  const int head = join.h * p.group + r - tok * p.group;
   const float inv = l == 0.f ? 0.f : 1.0f / l;
   *reinterpret_cast<uint2*>(p.out + row * p.out_stride + head * kHeadDim + lane * 4) =
       make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
@@ -901,8 +896,9 @@ __global__ void __launch_bounds__(kWThreads, 2)
   const int n_kt = (w.max_kv + kBN - 1) / kBN, n_sh = w.n_seqs * w.kv_heads;
   const int kt = n_kt - 1 - blockIdx.x / n_sh, sh = blockIdx.x % n_sh;
   const int h = sh % w.kv_heads, s = sh / w.kv_heads;
+  ptx::let_next_launch();
+  ptx::wait_previous();
   const PagedSeq q = paged_seq(w, s);
-  ptx::wait_previous();  // every thread, before any leaves: the weights follow the attention, also for later calls
   const int j0 = kt * kBN;
   if (!q.ok || q.n_q == 0 || j0 >= q.kv) return;  // a bad length was reported by the attention
   const int G = p.group;
@@ -1095,8 +1091,7 @@ cudaError_t launch_paged_chunk(const CUtensorMap& tm_q, const CUtensorMap& tm_k,
                                const PagedAttnParams& p, cudaStream_t stream) {
   cudaError_t err = configure();
   if (err != cudaSuccess) return err;
-  paged_plan_kernel<<<1, kPlanThreads, 0, stream>>>(p);
-  err = cudaGetLastError();
+  err = launch_after(paged_plan_kernel, 1, kPlanThreads, 0, stream, p);
   if (err == cudaSuccess)
     err = launch_after(paged_chunk_kernel, kSmCount, kThreads, kSmemBytes, stream, tm_q, tm_k, tm_v, p);
   if (err == cudaSuccess) err = launch_after(paged_join_kernel, kSmCount * kJoinSlices, kJoinThreads, 0, stream, p);

@@ -1,12 +1,13 @@
-// Attention over a paged cache when a stream brings few rows: at most 16 per KV head (a single
-// token of up to 16 grouped heads, a few drafted tokens of fewer).
+// Attention over a paged cache when a stream brings few rows: at most 32 per KV head (a single token of
+// grouped heads, a few drafted tokens).
 //
-// With R rows per KV head a cached token costs 512 bytes of K and V and 512 R multiply-adds, so
-// at 16 rows the memory asks for 16 flops a byte, a fraction of what even the warp-level matrix
-// instructions (mma.sync m16n8k16, whose 16 rows fit exactly) give: the kernel is bound by
-// HBM, and everything serves to keep loads in flight. One warp issues TMA copies of 64-token tiles (K
-// and V, one box per page and 64-column half) into three stages, four warps own 16 tokens of each tile and
-// run their own softmax in registers, without meeting each other until the unit's end, where the four
+// With R rows per KV head a cached token costs 512 bytes of K and V and 256 R multiply-adds: at 16 rows 16 flops
+// a byte, which the warp-level matrix instructions (mma.sync m16n8k16, 16 rows at a time; one in 32 clocks
+// per SM quarter here, 144 TFLOP/s in all) still outrun: the kernel is bound by HBM, and everything serves to
+// keep loads in flight. (At 32 rows they are the bound, at 64 the kernel took 40 us where the tcgen05 kernel
+// of rkv_paged_attention.cu takes 35: so far this form goes.) One warp issues TMA copies of 64-token tiles (K and V, one box per page and 64-column
+// half) into three stages; four warps share a tile: kRowTiles of 16 rows times 4 / kRowTiles runs of tokens.
+// Each runs its own softmax in registers, without meeting the others until the unit's end, where the runs'
 // partial results are merged through shared memory. Two thread blocks fit an SM: six stages of 32 KB
 // in flight.
 //
@@ -34,7 +35,7 @@ constexpr int kDecodeThreads = (kWarps + 1) * 32;
 constexpr int kMergeRows = kWarps;      // rows merged at a time, a warp each
 constexpr int kSmemMerge = kStages * kStageBytes;                              // [warp][row][128] floats
 constexpr int kSmemMl = kSmemMerge + kWarps * kMergeRows * kHeadDim * 4;       // [warp][row]: reference, sum
-constexpr int kSmemDecodeBar = kSmemMl + kWarps * 16 * 8;
+constexpr int kSmemDecodeBar = kSmemMl + 128 * 8;
 constexpr int kDecodeSmem = kSmemDecodeBar + 128 + 1024;
 constexpr int kMinTiles = 4;  // tiles of a share at least
 constexpr float kLn2 = 0.6931471805599453f;
@@ -163,6 +164,324 @@ struct TokenWalk {
   }
 };
 
+// One unit (or part) of a thread block's share, by the four consumer warps: kRowTiles tiles of 16 rows times
+// 4 / kRowTiles runs of each tile's tokens. g: tiles consumed before it; ok: no wait has expired (a warp whose
+// wait expires skips further work but still passes the barriers).
+template <int kRowTiles>
+__device__ __forceinline__ void token_unit(const PagedAttnParams& p, const TokenUnit& u, uint8_t* smem, uint64_t* full,
+                                           uint64_t* empty, int& g, bool& ok) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kRuns = kWarps / kRowTiles;       // warps that share a row tile
+  constexpr int kRun = kTileKeys / kRuns;         // tokens of a tile per warp
+  const int row_tile = warp % kRowTiles, run0 = warp / kRowTiles * kRun;
+  const int ra = row_tile * 16 + (lane >> 2), rb = ra + 8;  // this lane's two rows
+  const int cq = (lane & 3) * 2;                            // and its pair of columns within 8
+  const int tok_a = ra / p.group, tok_b = rb / p.group;
+  // ldmatrix rows: K by token (lanes 8-15: the next 8 columns, 16-31: the next 8 tokens), V by token
+  // (lanes 8-15: the next 8 tokens, 16-31: the next 8 columns)
+  const int krow = run0 + (lane >> 4) * 8 + (lane & 7), kcol = (lane >> 3) & 1;
+  const int vrow = run0 + ((lane >> 3) & 1) * 8 + (lane & 7), vcol = lane >> 4;
+  const uint32_t sbase = ptx::smem_u32(smem);
+  float* mo = reinterpret_cast<float*>(smem + kSmemMerge);
+  float2* ml = reinterpret_cast<float2*>(smem + kSmemMl);
+  const PagedSeq& q = u.q;
+  const int rows = q.n_q * p.group;
+  uint32_t qa[8][4];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int r = e ? rb : ra, tok = e ? tok_b : tok_a;
+    const bool live = r < rows;
+    const uint16_t* src = p.q + (q.q0 + (live ? tok : 0)) * p.q_stride + (u.h * p.group + r - tok * p.group) * kHeadDim;
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk) {
+      qa[kk][e] = live ? __ldg(reinterpret_cast<const uint32_t*>(src + kk * 16 + cq)) : 0u;
+      qa[kk][2 + e] = live ? __ldg(reinterpret_cast<const uint32_t*>(src + kk * 16 + 8 + cq)) : 0u;
+    }
+  }
+  // the last place each row sees
+  const int last_a = p.causal ? q.kv - q.n_q + tok_a : q.kv - 1;
+  const int last_b = p.causal ? q.kv - q.n_q + tok_b : q.kv - 1;
+  const int last_all = p.causal ? q.kv - q.n_q : q.kv - 1;
+  // where their scores go (a pair of places each), if they are kept
+  const long long score_a = (static_cast<long long>(q.q0 + tok_a) * p.q_heads + u.h * p.group + ra - tok_a * p.group) * p.score_stride + cq;
+  const long long score_b = (static_cast<long long>(q.q0 + tok_b) * p.q_heads + u.h * p.group + rb - tok_b * p.group) * p.score_stride + cq;
+  float o[16][4];
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) o[i][c] = 0.f;
+  float ma = kNoKey, mb = kNoKey, la = 0.f, lb = 0.f;  // references (log2) and this lane's sums
+  for (int t = u.t0; t < u.t1; ++t, ++g) {
+    const int st = g % kStages;
+    if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait(&full[st], (g / kStages) & 1, p.wait_limit_ns));
+    if (!ok) continue;
+    const uint32_t kt = sbase + st * kStageBytes, vt = kt + 2 * kHalf;
+    const int jw = t * kTileKeys + run0;  // this warp's first token
+    if (jw < q.kv && row_tile * 16 < rows) {
+      float sc[2 * kRowTiles][4];
+#pragma unroll
+      for (int i = 0; i < 2 * kRowTiles; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) sc[i][c] = 0.f;
+      if (kRowTiles == 1) {
+        // four chains of four products instead of two of eight: half the latency
+        float sd[2][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) sd[i][c] = 0.f;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          const int chunk = kk * 2 + kcol;  // 16-byte chunk of the row; 128-byte swizzle within a half
+          uint32_t b[4];
+          ptx::ldsm4(kt + (chunk >> 3) * kHalf + krow * 128 + (((chunk & 7) ^ (krow & 7)) << 4), b);
+          ptx::mma16816(kk & 1 ? sd[0] : sc[0], qa[kk], b[0], b[1]);
+          ptx::mma16816(kk & 1 ? sd[1] : sc[1], qa[kk], b[2], b[3]);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) sc[i][c] += sd[i][c];
+      } else {
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          const int chunk = kk * 2 + kcol;
+#pragma unroll
+          for (int i = 0; i < kRowTiles; ++i) {
+            uint32_t b[4];
+            ptx::ldsm4(kt + (chunk >> 3) * kHalf + (krow + 16 * i) * 128 + (((chunk & 7) ^ (krow & 7)) << 4), b);
+            ptx::mma16816(sc[2 * i], qa[kk], b[0], b[1]);
+            ptx::mma16816(sc[2 * i + 1], qa[kk], b[2], b[3]);
+          }
+        }
+      }
+      float xa = -INFINITY, xb = -INFINITY;
+      const bool ragged = jw + kRun - 1 > last_all;
+#pragma unroll
+      for (int i = 0; i < 2 * kRowTiles; ++i) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) sc[i][c] *= p.scale_log2;
+        if (ragged) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (jw + i * 8 + cq + (c & 1) > (c < 2 ? last_a : last_b)) sc[i][c] = -INFINITY;
+        }
+        xa = ptx::fmax3(xa, sc[i][0], sc[i][1]);
+        xb = ptx::fmax3(xb, sc[i][2], sc[i][3]);
+      }
+      if (kRowTiles == 1 && p.scores != nullptr) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (ra < rows)
+            *reinterpret_cast<float2*>(p.scores + score_a + jw + i * 8) = make_float2(sc[i][0], sc[i][1]);
+          if (rb < rows)
+            *reinterpret_cast<float2*>(p.scores + score_b + jw + i * 8) = make_float2(sc[i][2], sc[i][3]);
+        }
+      }
+      xa = fmaxf(xa, __shfl_xor_sync(0xffffffffu, xa, 1));
+      xb = fmaxf(xb, __shfl_xor_sync(0xffffffffu, xb, 1));
+      xa = fmaxf(xa, __shfl_xor_sync(0xffffffffu, xa, 2));
+      xb = fmaxf(xb, __shfl_xor_sync(0xffffffffu, xb, 2));
+      if (__any_sync(0xffffffffu, xa > ma + kRescale || xb > mb + kRescale)) {
+        const float na = fmaxf(ma, xa), nb = fmaxf(mb, xb);
+        const float fa = ptx::ex2(ma - na), fb = ptx::ex2(mb - nb);
+        ma = na;
+        mb = nb;
+        la *= fa;
+        lb *= fb;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          o[i][0] *= fa;
+          o[i][1] *= fa;
+          o[i][2] *= fb;
+          o[i][3] *= fb;
+        }
+      }
+      const bool cut = jw + kRun > q.kv;
+#pragma unroll
+      for (int i = 0; i < kRowTiles; ++i) {
+        // p in fp32 for the sum; rounded to bf16 for the product with V, the operand type of the
+        // matrix instruction (half a step, 2^-8, of each weight: the size of the output's own rounding)
+        float (&x)[4] = sc[2 * i];
+        float (&y)[4] = sc[2 * i + 1];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          x[c] = ptx::ex2(x[c] - (c < 2 ? ma : mb));
+          y[c] = ptx::ex2(y[c] - (c < 2 ? ma : mb));
+        }
+        la += (x[0] + x[1]) + (y[0] + y[1]);
+        lb += (x[2] + x[3]) + (y[2] + y[3]);
+        const uint32_t pa[4] = {pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(y[0], y[1]), pack2(y[2], y[3])};
+        // tokens past the end have p = 0, but their V may be anything: zero it
+        uint32_t k0 = 0xffffffffu, k1 = 0xffffffffu;
+        if (cut) {
+          const int v = q.kv - jw - 16 * i;
+          k0 = (cq < v ? 0xffffu : 0u) | (cq + 1 < v ? 0xffff0000u : 0u);
+          k1 = (cq + 8 < v ? 0xffffu : 0u) | (cq + 9 < v ? 0xffff0000u : 0u);
+        }
+#pragma unroll
+        for (int np = 0; np < 8; ++np) {
+          const int chunk = np * 2 + vcol;
+          uint32_t b[4];
+          ptx::ldsm4_t(vt + (chunk >> 3) * kHalf + (vrow + 16 * i) * 128 + (((chunk & 7) ^ (vrow & 7)) << 4), b);
+          if (cut) {
+            b[0] &= k0;
+            b[1] &= k1;
+            b[2] &= k0;
+            b[3] &= k1;
+          }
+          ptx::mma16816(o[2 * np], pa, b[0], b[1]);
+          ptx::mma16816(o[2 * np + 1], pa, b[2], b[3]);
+        }
+      }
+    }
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(&empty[st]);
+  }
+
+  // ------------------------------------------------------------ merge of the runs
+  la += __shfl_xor_sync(0xffffffffu, la, 1);
+  lb += __shfl_xor_sync(0xffffffffu, lb, 1);
+  la += __shfl_xor_sync(0xffffffffu, la, 2);
+  lb += __shfl_xor_sync(0xffffffffu, lb, 2);
+  const bool whole = u.t0 == 0 && u.t1 == u.tiles;
+  // a part: this thread block's first slot if the unit began before its share, else its second
+  const long long slot = (2LL * blockIdx.x + (u.t0 == 0 ? 1 : 0)) * p.slot_rows;
+  if (kRowTiles == 2) {
+    // the second run's warp holds the same rows and columns lane by lane: half of them at a time
+    float2* far = reinterpret_cast<float2*>(mo) + row_tile * 16 * 32 + lane;
+    if (warp >= kRowTiles) {
+      ml[row_tile * 64 + lane] = make_float2(ma, la);
+      ml[row_tile * 64 + 32 + lane] = make_float2(mb, lb);
+    }
+    float ga = 0.f, gb = 0.f;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      if (warp >= kRowTiles) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          far[(2 * i) * 32] = make_float2(o[half * 8 + i][0], o[half * 8 + i][1]);
+          far[(2 * i + 1) * 32] = make_float2(o[half * 8 + i][2], o[half * 8 + i][3]);
+        }
+      }
+      ptx::named_bar_sync(1, kWarps * 32);
+      if (warp < kRowTiles) {
+        if (half == 0) {
+          const float2 ea = ml[row_tile * 64 + lane], eb = ml[row_tile * 64 + 32 + lane];
+          const float na = fmaxf(ma, ea.x), nb = fmaxf(mb, eb.x);
+          const float fa = ptx::ex2(ma - na), fb = ptx::ex2(mb - nb);
+          ga = ptx::ex2(ea.x - na);
+          gb = ptx::ex2(eb.x - nb);
+          ma = na;
+          mb = nb;
+          la = la * fa + ea.y * ga;
+          lb = lb * fb + eb.y * gb;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            o[i][0] *= fa;
+            o[i][1] *= fa;
+            o[i][2] *= fb;
+            o[i][3] *= fb;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float2 x = far[(2 * i) * 32], y = far[(2 * i + 1) * 32];
+          o[half * 8 + i][0] += x.x * ga;
+          o[half * 8 + i][1] += x.y * ga;
+          o[half * 8 + i][2] += y.x * gb;
+          o[half * 8 + i][3] += y.y * gb;
+        }
+      }
+      ptx::named_bar_sync(1, kWarps * 32);
+    }
+    if (ok && warp < kRowTiles) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = e ? rb : ra, tok = e ? tok_b : tok_a;
+        if (r >= rows) continue;
+        const float m = e ? mb : ma, l = e ? lb : la;
+        if (whole) {
+          const long long row = q.q0 + tok;
+          const int head = u.h * p.group + r - tok * p.group;
+          const float inv = l == 0.f ? 0.f : 1.0f / l;
+          uint16_t* to = p.out + row * p.out_stride + head * kHeadDim + cq;
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            *reinterpret_cast<uint32_t*>(to + i * 8) = pack2(o[i][2 * e] * inv, o[i][2 * e + 1] * inv);
+          if (cq == 0) {
+            const float z = l > 0.f ? m + log2f(l) : l == 0.f ? -INFINITY : l;
+            const long long rh = row * p.q_heads + head;
+            if (p.lse != nullptr) p.lse[rh] = z * kLn2;
+            if (p.lse2 != nullptr) p.lse2[rh] = z;
+          }
+        } else {
+          float* to = p.part + (slot + r) * kHeadDim + cq;
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            *reinterpret_cast<float2*>(to + i * 8) = make_float2(o[i][2 * e], o[i][2 * e + 1]);
+          if (cq == 0) p.part_ml[slot + r] = make_float2(m, l);
+        }
+      }
+    }
+    return;
+  }
+  if ((lane & 3) == 0) {
+    ml[warp * 16 + ra] = make_float2(ma, la);
+    ml[warp * 16 + rb] = make_float2(mb, lb);
+  }
+#pragma unroll
+  for (int rg = 0; rg < 16 / kMergeRows; ++rg) {
+    if (rg * kMergeRows >= rows) break;
+    // lanes 16 (rg & 1) .. + 15 hold these rows, in their first or second half
+    if ((lane >> 4) == (rg & 1)) {
+      float* to = mo + (warp * kMergeRows + (ra & (kMergeRows - 1))) * kHeadDim + cq;
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        *reinterpret_cast<float2*>(to + i * 8) = make_float2(o[i][rg & 2], o[i][(rg & 2) + 1]);
+    }
+    ptx::named_bar_sync(1, kWarps * 32);
+    const int r = rg * kMergeRows + warp, c = lane * 4;  // a warp per row
+    if (ok && r < rows) {
+      float m = kNoKey;
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) m = fmaxf(m, ml[i * 16 + r].x);
+      float l = 0.f;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) {
+        const float2 e = ml[i * 16 + r];
+        const float f = ptx::ex2(e.x - m);
+        const float4 y = *reinterpret_cast<const float4*>(mo + (i * kMergeRows + warp) * kHeadDim + c);
+        l += e.y * f;
+        x.x += y.x * f;
+        x.y += y.y * f;
+        x.z += y.z * f;
+        x.w += y.w * f;
+      }
+      if (whole) {
+        const int tok = r / p.group;
+        const long long row = q.q0 + tok;
+        const int head = u.h * p.group + r - tok * p.group;
+        const float inv = l == 0.f ? 0.f : 1.0f / l;
+        *reinterpret_cast<uint2*>(p.out + row * p.out_stride + head * kHeadDim + c) =
+            make_uint2(pack2(x.x * inv, x.y * inv), pack2(x.z * inv, x.w * inv));
+        if (lane == 0) {
+          const float z = l > 0.f ? m + log2f(l) : l == 0.f ? -INFINITY : l;
+          const long long rh = row * p.q_heads + head;
+          if (p.lse != nullptr) p.lse[rh] = z * kLn2;
+          if (p.lse2 != nullptr) p.lse2[rh] = z;
+        }
+      } else {
+        *reinterpret_cast<float4*>(p.part + (slot + r) * kHeadDim + c) = x;
+        if (lane == 0) p.part_ml[slot + r] = make_float2(m, l);
+      }
+    }
+    ptx::named_bar_sync(1, kWarps * 32);
+  }
+}
+
+template <int kMaxRowTiles>
 __global__ void __launch_bounds__(kDecodeThreads, 2)
     paged_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                         const __grid_constant__ PagedAttnParams p) {
@@ -181,6 +500,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
     }
     ptx::fence_mbar_init();
   }
+  ptx::wait_previous();
   TokenWalk walk;
   walk.count(w);
   if (cta >= walk.n) {
@@ -238,209 +558,15 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
   }
 
   // -------------------------------------------------------------- consumers
-  const int ra = lane >> 2, rb = ra + 8;  // this lane's two rows
-  const int cq = (lane & 3) * 2;          // and its pair of columns within 8
-  const int tok_a = ra / p.group, tok_b = rb / p.group;
-  // ldmatrix rows: K by token (lanes 8-15: the next 8 columns, 16-31: the next 8 tokens), V by token
-  // (lanes 8-15: the next 8 tokens, 16-31: the next 8 columns)
-  const int krow = warp * 16 + (lane >> 4) * 8 + (lane & 7), kcol = (lane >> 3) & 1;
-  const int vrow = warp * 16 + ((lane >> 3) & 1) * 8 + (lane & 7), vcol = lane >> 4;
-  const uint32_t sbase = ptx::smem_u32(smem);
-  float* mo = reinterpret_cast<float*>(smem + kSmemMerge);
-  float2* ml = reinterpret_cast<float2*>(smem + kSmemMl);
-  bool ok = true;  // after an expired wait a warp skips further work but still passes the barriers
+  // a unit takes the fewest row tiles that hold its rows: with few rows all four warps share the tokens
+  bool ok = true;
   int g = 0;
   while (walk.next(w, u)) {
-    const PagedSeq& q = u.q;
-    const int rows = q.n_q * p.group;
-    uint32_t qa[8][4];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int r = e ? rb : ra, tok = e ? tok_b : tok_a;
-      const bool live = r < rows;
-      const uint16_t* src = p.q + (q.q0 + (live ? tok : 0)) * p.q_stride + (u.h * p.group + r - tok * p.group) * kHeadDim;
-#pragma unroll
-      for (int kk = 0; kk < 8; ++kk) {
-        qa[kk][e] = live ? __ldg(reinterpret_cast<const uint32_t*>(src + kk * 16 + cq)) : 0u;
-        qa[kk][2 + e] = live ? __ldg(reinterpret_cast<const uint32_t*>(src + kk * 16 + 8 + cq)) : 0u;
-      }
-    }
-    // the last place each row sees
-    const int last_a = p.causal ? q.kv - q.n_q + tok_a : q.kv - 1;
-    const int last_b = p.causal ? q.kv - q.n_q + tok_b : q.kv - 1;
-    const int last_all = p.causal ? q.kv - q.n_q : q.kv - 1;
-    // where their scores go (a pair of places each), if they are kept
-    const long long score_a = (static_cast<long long>(q.q0 + tok_a) * p.q_heads + u.h * p.group + ra - tok_a * p.group) * p.score_stride + cq;
-    const long long score_b = (static_cast<long long>(q.q0 + tok_b) * p.q_heads + u.h * p.group + rb - tok_b * p.group) * p.score_stride + cq;
-    float o[16][4];
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) o[i][c] = 0.f;
-    float ma = kNoKey, mb = kNoKey, la = 0.f, lb = 0.f;  // references (log2) and this lane's sums
-    for (int t = u.t0; t < u.t1; ++t, ++g) {
-      const int st = g % kStages;
-      if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait(&full[st], (g / kStages) & 1, p.wait_limit_ns));
-      if (!ok) continue;
-      const uint32_t kt = sbase + st * kStageBytes, vt = kt + 2 * kHalf;
-      const int jw = t * kTileKeys + warp * 16;  // this warp's first token
-      if (jw < q.kv) {
-        // four chains of four products: the scores' latency is half the tile's
-        float sc[2][4], sd[2][4];
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) sc[i][c] = sd[i][c] = 0.f;
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          const int chunk = kk * 2 + kcol;  // 16-byte chunk of the row; 128-byte swizzle within a half
-          uint32_t b[4];
-          ptx::ldsm4(kt + (chunk >> 3) * kHalf + krow * 128 + (((chunk & 7) ^ (krow & 7)) << 4), b);
-          ptx::mma16816(kk & 1 ? sd[0] : sc[0], qa[kk], b[0], b[1]);
-          ptx::mma16816(kk & 1 ? sd[1] : sc[1], qa[kk], b[2], b[3]);
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) sc[i][c] = (sc[i][c] + sd[i][c]) * p.scale_log2;
-        if (jw + 15 > last_all) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              if (jw + i * 8 + cq + (c & 1) > (c < 2 ? last_a : last_b)) sc[i][c] = -INFINITY;
-        }
-        if (p.scores != nullptr) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            if (ra < rows)
-              *reinterpret_cast<float2*>(p.scores + score_a + jw + i * 8) = make_float2(sc[i][0], sc[i][1]);
-            if (rb < rows)
-              *reinterpret_cast<float2*>(p.scores + score_b + jw + i * 8) = make_float2(sc[i][2], sc[i][3]);
-          }
-        }
-        float xa = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));
-        float xb = fmaxf(fmaxf(sc[0][2], sc[0][3]), fmaxf(sc[1][2], sc[1][3]));
-        xa = fmaxf(xa, __shfl_xor_sync(0xffffffffu, xa, 1));
-        xb = fmaxf(xb, __shfl_xor_sync(0xffffffffu, xb, 1));
-        xa = fmaxf(xa, __shfl_xor_sync(0xffffffffu, xa, 2));
-        xb = fmaxf(xb, __shfl_xor_sync(0xffffffffu, xb, 2));
-        if (__any_sync(0xffffffffu, xa > ma + kRescale || xb > mb + kRescale)) {
-          const float na = fmaxf(ma, xa), nb = fmaxf(mb, xb);
-          const float fa = ptx::ex2(ma - na), fb = ptx::ex2(mb - nb);
-          ma = na;
-          mb = nb;
-          la *= fa;
-          lb *= fb;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            o[i][0] *= fa;
-            o[i][1] *= fa;
-            o[i][2] *= fb;
-            o[i][3] *= fb;
-          }
-        }
-        // p in fp32 for the sum; rounded to bf16 for the product with V, the operand type of the
-        // matrix instruction (half a step, 2^-8, of each weight: the size of the output's own rounding)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          sc[i][0] = ptx::ex2(sc[i][0] - ma);
-          sc[i][1] = ptx::ex2(sc[i][1] - ma);
-          sc[i][2] = ptx::ex2(sc[i][2] - mb);
-          sc[i][3] = ptx::ex2(sc[i][3] - mb);
-          la += sc[i][0] + sc[i][1];
-          lb += sc[i][2] + sc[i][3];
-        }
-        const uint32_t pa[4] = {pack2(sc[0][0], sc[0][1]), pack2(sc[0][2], sc[0][3]), pack2(sc[1][0], sc[1][1]),
-                                pack2(sc[1][2], sc[1][3])};
-        // tokens past the end have p = 0, but their V may be anything: zero it
-        uint32_t k0 = 0xffffffffu, k1 = 0xffffffffu;
-        const bool cut = jw + 16 > q.kv;
-        if (cut) {
-          const int v = q.kv - jw;
-          k0 = (cq < v ? 0xffffu : 0u) | (cq + 1 < v ? 0xffff0000u : 0u);
-          k1 = (cq + 8 < v ? 0xffffu : 0u) | (cq + 9 < v ? 0xffff0000u : 0u);
-        }
-#pragma unroll
-        for (int np = 0; np < 8; ++np) {
-          const int chunk = np * 2 + vcol;
-          uint32_t b[4];
-          ptx::ldsm4_t(vt + (chunk >> 3) * kHalf + vrow * 128 + (((chunk & 7) ^ (vrow & 7)) << 4), b);
-          if (cut) {
-            b[0] &= k0;
-            b[1] &= k1;
-            b[2] &= k0;
-            b[3] &= k1;
-          }
-          ptx::mma16816(o[2 * np], pa, b[0], b[1]);
-          ptx::mma16816(o[2 * np + 1], pa, b[2], b[3]);
-        }
-      }
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&empty[st]);
-    }
-
-    // ------------------------------------------------------------ merge of the four warps
-    la += __shfl_xor_sync(0xffffffffu, la, 1);
-    lb += __shfl_xor_sync(0xffffffffu, lb, 1);
-    la += __shfl_xor_sync(0xffffffffu, la, 2);
-    lb += __shfl_xor_sync(0xffffffffu, lb, 2);
-    if ((lane & 3) == 0) {
-      ml[warp * 16 + ra] = make_float2(ma, la);
-      ml[warp * 16 + rb] = make_float2(mb, lb);
-    }
-    const bool whole = u.t0 == 0 && u.t1 == u.tiles;
-    // a part: this thread block's first slot if the unit began before its share, else its second
-    const long long slot = (2LL * cta + (u.t0 == 0 ? 1 : 0)) * kPagedRows;
-#pragma unroll
-    for (int rg = 0; rg < kPagedRows / kMergeRows; ++rg) {
-      if (rg * kMergeRows >= rows) break;
-      // lanes 16 (rg & 1) .. + 15 hold these rows, in their first or second half
-      if ((lane >> 4) == (rg & 1)) {
-        float* to = mo + (warp * kMergeRows + (ra & (kMergeRows - 1))) * kHeadDim + cq;
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          *reinterpret_cast<float2*>(to + i * 8) = make_float2(o[i][rg & 2], o[i][(rg & 2) + 1]);
-      }
-      ptx::named_bar_sync(1, kWarps * 32);
-      const int r = rg * kMergeRows + warp, c = lane * 4;  // a warp per row
-      if (ok && r < rows) {
-        float m = kNoKey;
-#pragma unroll
-        for (int i = 0; i < kWarps; ++i) m = fmaxf(m, ml[i * 16 + r].x);
-        float l = 0.f;
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int i = 0; i < kWarps; ++i) {
-          const float2 e = ml[i * 16 + r];
-          const float f = ptx::ex2(e.x - m);
-          const float4 y = *reinterpret_cast<const float4*>(mo + (i * kMergeRows + warp) * kHeadDim + c);
-          l += e.y * f;
-          x.x += y.x * f;
-          x.y += y.y * f;
-          x.z += y.z * f;
-          x.w += y.w * f;
-        }
-        if (whole) {
-          const int tok = r / p.group;
-          const long long row = q.q0 + tok;
-          const int head = u.h * p.group + r - tok * p.group;
-          const float inv = l == 0.f ? 0.f : 1.0f / l;
-          *reinterpret_cast<uint2*>(p.out + row * p.out_stride + head * kHeadDim + c) =
-              make_uint2(pack2(x.x * inv, x.y * inv), pack2(x.z * inv, x.w * inv));
-          if (lane == 0) {
-            const float z = l > 0.f ? m + log2f(l) : l == 0.f ? -INFINITY : l;
-            const long long rh = row * p.q_heads + head;
-            if (p.lse != nullptr) p.lse[rh] = z * kLn2;
-            if (p.lse2 != nullptr) p.lse2[rh] = z;
-          }
-        } else {
-          *reinterpret_cast<float4*>(p.part + (slot + r) * kHeadDim + c) = x;
-          if (lane == 0) p.part_ml[slot + r] = make_float2(m, l);
-        }
-      }
-      ptx::named_bar_sync(1, kWarps * 32);
-    }
+    const int rows = u.q.n_q * p.group;
+    if (kMaxRowTiles == 1 || rows <= 16)
+      token_unit<1>(p, u, smem, full, empty, g, ok);
+    else
+      token_unit<2>(p, u, smem, full, empty, g, ok);
   }
   if (!ok && lane == 0) paged_report(w, kStatusTimeout);
 }
@@ -453,7 +579,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
 // A block takes 64 columns; sixteen lanes hold a row's, so a warp reads two parts at once, and the warps that
 // the unit's rows leave over (two per row for 8 rows, four for 4) take their share of the parts: all loads
 // leave together. (A warp per row, part after part: 13 us of 96 for 8 rows in 37 parts.)
-constexpr int kTokenJoinWarps = kPagedRows;
+constexpr int kTokenJoinWarps = 16;  // of 16 rows a block; more rows take more blocks
 
 __global__ void __launch_bounds__(kTokenJoinWarps * 32)
     paged_token_join_kernel(const __grid_constant__ PagedAttnParams p) {
@@ -461,10 +587,11 @@ __global__ void __launch_bounds__(kTokenJoinWarps * 32)
   __shared__ float2 sum_ml[kTokenJoinWarps];
   ptx::let_next_launch();
   const int c = blockIdx.x / 2 + 1, col = (blockIdx.x & 1) * 64 + (threadIdx.x & 15) * 4;
+  const int row0 = blockIdx.y * 16;
   ptx::wait_previous();  // in every thread block, so that the kernel after this one may rely on it
   const PagedCut cut = p.cuts[c];
-  const int rows = cut.n_q * p.group;
-  if (rows == 0) return;
+  const int rows = min(16, cut.n_q * p.group - row0);  // of this block
+  if (rows <= 0) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int teams = kTokenJoinWarps / rows;
   const int r = warp % rows, team = warp / rows;
@@ -483,7 +610,7 @@ __global__ void __launch_bounds__(kTokenJoinWarps * 32)
   if (team < teams) {
 #pragma unroll 4
     for (int i = team * 2 + (lane >> 4); i < cut.parts; i += teams * 2) {
-      const long long at = (i == 0 ? 2LL * c - 1 : 2LL * (c - 1 + i)) * kPagedRows + r;
+      const long long at = (i == 0 ? 2LL * c - 1 : 2LL * (c - 1 + i)) * p.slot_rows + row0 + r;
       add(p.part_ml[at], *reinterpret_cast<const float4*>(p.part + at * kHeadDim + col));
     }
   }
@@ -501,9 +628,9 @@ __global__ void __launch_bounds__(kTokenJoinWarps * 32)
   __syncthreads();
   if (team != 0 || lane >= 16) return;
   for (int i = 1; i < teams; ++i) add(sum_ml[i * rows + r], sum[i * rows + r][lane]);
-  const int tok = r / p.group;
+  const int tok = (row0 + r) / p.group;
   const long long row = cut.row0 + tok;
-  const int head = cut.h * p.group + r - tok * p.group;
+  const int head = cut.h * p.group + row0 + r - tok * p.group;
   const float inv = l == 0.f ? 0.f : 1.0f / l;
   *reinterpret_cast<uint2*>(p.out + row * p.out_stride + head * kHeadDim + col) =
       make_uint2(pack2(o.x * inv, o.y * inv), pack2(o.z * inv, o.w * inv));
@@ -582,15 +709,18 @@ cudaError_t launch_paged_decode(const CUtensorMap& tm_k, const CUtensorMap& tm_v
   {
     std::lock_guard<std::mutex> lock(mu);
     if (!configured[dev]) {
-      err = cudaFuncSetAttribute(paged_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kDecodeSmem);
+      constexpr auto kAttr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+      err = cudaFuncSetAttribute(paged_decode_kernel<1>, kAttr, kDecodeSmem);
+      if (err == cudaSuccess) err = cudaFuncSetAttribute(paged_decode_kernel<2>, kAttr, kDecodeSmem);
       if (err != cudaSuccess) return err;
       configured[dev] = true;
     }
   }
-  paged_decode_kernel<<<2 * kSmCount, kDecodeThreads, kDecodeSmem, stream>>>(tm_k, tm_v, p);
-  err = cudaGetLastError();
+  const auto kernel = p.slot_rows == 16 ? paged_decode_kernel<1> : paged_decode_kernel<2>;
+  err = launch_after(kernel, 2 * kSmCount, kDecodeThreads, kDecodeSmem, stream, tm_k, tm_v, p);
   if (err != cudaSuccess) return err;
-  return launch_after(paged_token_join_kernel, 2 * (2 * kSmCount - 1), kTokenJoinWarps * 32, 0, stream, p);
+  const dim3 joins(2 * (2 * kSmCount - 1), static_cast<unsigned>(p.slot_rows / 16));
+  return launch_after(paged_token_join_kernel, joins, kTokenJoinWarps * 32, 0, stream, p);
 }
 
 }  // namespace rkv

@@ -85,15 +85,17 @@ int check_heads(const rkv_page_pool* pool, int q_heads, int n_rows) {
   return RKV_OK;
 }
 
-// Which form a call takes, and its workspace. The single-token form serves up to 16 rows per stream and KV
-// head, which fill one warp-level matrix instruction; above that the chunk form's tiles of 128 rows
-// are the better use (17 rows: both are bound by HBM).
+// Which form a call takes, and its workspace. The single-token form (warp-level matrix instructions, bound by
+// HBM) serves up to 32 rows per stream and KV head; above that the chunk form's tiles of 128 rows are the
+// better use (the measurements stand in rkv_paged_decode.cu).
 rkv::PagedPlan plan_of(const rkv_page_pool* pool, const rkv_paged_batch* b, int q_heads, int n_rows, bool weight) {
   rkv::PagedPlan p;
   std::memset(&p, 0, sizeof(p));
   const int group = q_heads / pool->kv_heads;
-  p.rows_form = static_cast<long long>(b->max_q) * group <= rkv::kPagedRows;
-  if (!p.rows_form) {
+  const long long most = static_cast<long long>(b->max_q) * group;
+  if (most <= rkv::kPagedRows) {
+    p.slot_rows = most <= 16 ? 16 : 32;
+  } else {
     p.block_tokens = 2 * (rkv::kQueryBox / group);
     const long long per_seq = (static_cast<long long>(b->max_q) + p.block_tokens - 1) / p.block_tokens;
     p.n_blocks = static_cast<int>(std::min(static_cast<long long>(n_rows) / p.block_tokens + b->n_seqs,
@@ -112,10 +114,10 @@ rkv::PagedPlan plan_of(const rkv_page_pool* pool, const rkv_paged_batch* b, int 
   };
   p.lse = weight ? take(4 * heads) : -1;
   p.cuts = p.blocks = p.work = p.seq_first = -1;
-  const long long rows = p.rows_form ? 4LL * rkv::kSmCount * rkv::kPagedRows : 2LL * rkv::kSmCount * rkv::kPagedPartRows;
+  const long long rows = p.slot_rows ? 4LL * rkv::kSmCount * p.slot_rows : 2LL * rkv::kSmCount * rkv::kPagedPartRows;
   p.part = take(4 * rows * kHeadDim);
   p.part_ml = take(8 * rows);
-  if (p.rows_form) {
+  if (p.slot_rows) {
     p.cuts = take(2LL * rkv::kSmCount * sizeof(rkv::PagedCut));
   } else {
     p.blocks = take(static_cast<long long>(sizeof(rkv::PagedBlock)) * p.n_blocks);
@@ -123,7 +125,8 @@ rkv::PagedPlan plan_of(const rkv_page_pool* pool, const rkv_paged_batch* b, int 
     p.seq_first = take(4LL * b->n_seqs);
   }
   p.score_stride = (b->max_kv + 63LL) / 64 * 64;
-  p.scores = weight && p.rows_form ? take(4 * heads * p.score_stride) : -1;
+  // scores are kept for at most 16 rows: 8 bytes of traffic for each, where reading K again takes 256
+  p.scores = weight && p.slot_rows == 16 ? take(4 * heads * p.score_stride) : -1;
   return p;
 }
 
@@ -219,23 +222,29 @@ RKV_API int rkv_paged_attention(const rkv_page_pool* pool, const rkv_paged_batch
   }
   if (plan.scores >= 0) p.scores = reinterpret_cast<float*>(ws + plan.scores);
   p.score_stride = plan.score_stride;
+  p.slot_rows = plan.slot_rows;
   p.block_tokens = plan.block_tokens;
   p.n_blocks = plan.n_blocks;
   p.wait_limit_ns = kWaitNs;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t err;
   CUtensorMap tm_q, tm_k, tm_v;
-  const int tile = plan.rows_form ? rkv::kPagedDecodeTile : rkv::kKeyBox;
+  const int tile = plan.slot_rows ? rkv::kPagedDecodeTile : rkv::kKeyBox;
+  const bool weigh = weight != nullptr && batch->max_kv > 0, from_scores = plan.scores >= 0;
   if (!encode_pages(&tm_k, pool->k, pool, tile) || !encode_pages(&tm_v, pool->v, pool, tile)) return RKV_ERR_CUDA;
-  if (plan.rows_form) {
-    err = rkv::launch_paged_decode(tm_k, tm_v, p, st);
-    if (err == cudaSuccess && weight != nullptr && batch->max_kv > 0) err = rkv::launch_paged_token_weight(p, st);
-  } else {
+  if (!plan.slot_rows || (weigh && !from_scores)) {
     if (!rkv::encode_map(&tm_q, q, q_heads, n_rows, kHeadDim * 2, static_cast<uint64_t>(q_stride) * 2, p.group,
                          rkv::kQueryBox / p.group))
       return RKV_ERR_CUDA;
-    err = rkv::launch_paged_chunk(tm_q, tm_k, tm_v, p, st);
-    if (err == cudaSuccess && weight != nullptr && batch->max_kv > 0) err = rkv::launch_paged_weight(tm_q, tm_k, p, st);
+  }
+  err = plan.slot_rows ? rkv::launch_paged_decode(tm_k, tm_v, p, st) : rkv::launch_paged_chunk(tm_q, tm_k, tm_v, p, st);
+  if (err == cudaSuccess && weigh) {
+    if (from_scores) {
+      err = rkv::launch_paged_token_weight(p, st);
+    } else {
+      if (plan.slot_rows && !encode_pages(&tm_k, pool->k, pool, rkv::kKeyBox)) return RKV_ERR_CUDA;
+      err = rkv::launch_paged_weight(tm_q, tm_k, p, st);
+    }
   }
   return cuda_rc(err);
 }
