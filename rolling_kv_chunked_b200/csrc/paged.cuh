@@ -83,4 +83,85 @@ __device__ __forceinline__ long long paged_offset(const PagedView& w, int id, in
          (static_cast<long long>(h) * (1 << w.page_shift) + slot) * kHeadDim;
 }
 
+// x / y where both nearly always fit 32 bits (a 64-bit division is some 100 instructions).
+__device__ __forceinline__ long long quotient(long long x, int y) {
+  return (x >> 32) == 0 ? static_cast<long long>(static_cast<unsigned>(x) / static_cast<unsigned>(y)) : x / y;
+}
+
+// Tiles of kTokens cached tokens of one KV head of a stream: none without rows, one (all masked) if nothing is
+// cached.
+template <int kTokens>
+__device__ __forceinline__ int paged_seq_tiles(const PagedSeq& q) {
+  return q.ok && q.n_q > 0 ? max(1, (q.kv + kTokens - 1) / kTokens) : 0;
+}
+
+// All tiles of the batch, stream after stream (in the order of `order`, if it is set) and head after head, and a
+// place among them. Whole warps call these.
+template <int kTokens>
+struct PagedTiles {
+  const int* order = nullptr;
+  long long all;
+  int s, h, t;  // the place: stream, head, tile
+  PagedSeq q;   // its stream
+  int tiles;    // and that stream's tiles of one head
+  int q0, n_q, kv, mine;  // lane l: stream l of the first 32, and its tiles
+
+  __device__ __forceinline__ int nth(int i) const { return order != nullptr ? order[i] : i; }
+  __device__ __forceinline__ void count(const PagedView& w, bool report) {
+    const int lane = threadIdx.x & 31;
+    all = 0;
+    mine = 0;
+    for (int base = 0; base < w.n_seqs; base += 32) {
+      int x = 0;
+      if (base + lane < w.n_seqs) {
+        const PagedSeq y = paged_seq(w, nth(base + lane));
+        if (!y.ok && report) paged_report(w, kStatusLength);
+        x = paged_seq_tiles<kTokens>(y);
+        if (base == 0) {
+          q0 = y.q0;
+          n_q = y.n_q;
+          kv = y.kv;
+          mine = x;
+        }
+      }
+      all += __reduce_add_sync(0xffffffffu, x);
+    }
+    all *= w.kv_heads;
+  }
+  // to tile x < all
+  __device__ __forceinline__ void go_to(const PagedView& w, long long x) {
+    const int lane = threadIdx.x & 31;
+    long long before = 0;
+    for (int base = 0; base < w.n_seqs; base += 32) {
+      const int c = base == 0 ? mine : base + lane < w.n_seqs ? paged_seq_tiles<kTokens>(paged_seq(w, nth(base + lane))) : 0;
+      int inc = c;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, inc, d);
+        if (lane >= d) inc += y;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, (before + inc) * w.kv_heads > x);
+      if (hit) {
+        const int l = __ffs(hit) - 1;
+        s = nth(base + l);
+        before += __shfl_sync(0xffffffffu, inc - c, l);
+        tiles = __shfl_sync(0xffffffffu, c, l);
+        if (base == 0) {
+          q.q0 = __shfl_sync(0xffffffffu, q0, l);
+          q.n_q = __shfl_sync(0xffffffffu, n_q, l);
+          q.kv = __shfl_sync(0xffffffffu, kv, l);
+          q.ok = true;
+        } else {
+          q = paged_seq(w, s);
+        }
+        break;
+      }
+      before += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    const long long in = x - before * w.kv_heads;
+    h = static_cast<int>(quotient(in, tiles));
+    t = static_cast<int>(in - static_cast<long long>(h) * tiles);
+  }
+};
+
 }  // namespace rkv

@@ -151,7 +151,7 @@ struct PagedPlan {
   int slot_rows;     // single-token form: rows of a stream and KV head, rounded up to 16 or 32; 0: chunk form
   int block_tokens;  // chunk form: tokens of one unit of rows
   int n_blocks;      // and such units of one KV head in the batch at most
-  long long lse, part, part_ml, scores, cuts, blocks, work, seq_first, total;  // -1: not used
+  long long lse, part, part_ml, scores, cuts, blocks, work, seq_first, order, ticket, total;  // -1: not used
   long long score_stride;
 };
 
@@ -195,6 +195,7 @@ struct PagedWork {
 struct PagedCut {
   int row0, n_q, h, parts;
 };
+constexpr int kPagedMaxOrder = 1024;  // streams that the plan puts in order at most
 constexpr int kPagedPartRows = 256;  // rows of a partial result of the chunk form
 
 struct PagedAttnParams {
@@ -214,7 +215,9 @@ struct PagedAttnParams {
   PagedCut* cuts;      // single-token form: [2 * kSmCount]
   PagedBlock* blocks;  // chunk form: [n_blocks]
   PagedWork* work;
+  unsigned* ticket;    // units that the chunks' weight kernel has drawn
   int* seq_first;      // chunk form: [n_seqs], the stream's first block
+  int* order;          // chunk form: [n_seqs], the streams by falling chunk length; null: as they come
   float* scores;    // [n_rows][q_heads][score_stride]: log2 scores of the single-token form; null: not kept
   long long score_stride;
   int slot_rows;                // single-token form

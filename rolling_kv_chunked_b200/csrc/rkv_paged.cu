@@ -10,8 +10,10 @@ namespace rkv {
 namespace {
 
 // ---------------------------------------------------------------- write
-// One warp per chunk row; 16 lanes move one head vector of K and V (16 bytes each).
+// One warp per chunk row; 16 lanes move one head vector of K and V (16 bytes each), four pairs of heads on
+// their way at once.
 constexpr int kWriteWarps = 4;
+constexpr int kWriteBatch = 4;
 
 __global__ void __launch_bounds__(kWriteWarps * 32) paged_write_kernel(const __grid_constant__ PagedWriteParams p) {
   const PagedView& w = p.view;
@@ -32,12 +34,25 @@ __global__ void __launch_bounds__(kWriteWarps * 32) paged_write_kernel(const __g
   if (id < 0) return;
   const int slot = pos & ((1 << w.page_shift) - 1);
   const int c = (lane & 15) * 8;
-  for (int h = lane >> 4; h < w.kv_heads; h += 2) {
-    const uint4 kx = __ldg(reinterpret_cast<const uint4*>(p.k + row * p.k_stride + h * kHeadDim + c));
-    const uint4 vx = __ldg(reinterpret_cast<const uint4*>(p.v + row * p.v_stride + h * kHeadDim + c));
-    const long long to = paged_offset(w, id, h, slot) + c;
-    *reinterpret_cast<uint4*>(w.k + to) = kx;
-    *reinterpret_cast<uint4*>(w.v + to) = vx;
+  for (int h0 = lane >> 4; h0 < w.kv_heads; h0 += 2 * kWriteBatch) {
+    uint4 kx[kWriteBatch], vx[kWriteBatch];
+#pragma unroll
+    for (int i = 0; i < kWriteBatch; ++i) {
+      const int h = h0 + 2 * i;
+      if (h < w.kv_heads) {
+        kx[i] = __ldg(reinterpret_cast<const uint4*>(p.k + row * p.k_stride + h * kHeadDim + c));
+        vx[i] = __ldg(reinterpret_cast<const uint4*>(p.v + row * p.v_stride + h * kHeadDim + c));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kWriteBatch; ++i) {
+      const int h = h0 + 2 * i;
+      if (h < w.kv_heads) {
+        const long long to = paged_offset(w, id, h, slot) + c;
+        *reinterpret_cast<uint4*>(w.k + to) = kx[i];
+        *reinterpret_cast<uint4*>(w.v + to) = vx[i];
+      }
+    }
   }
 }
 

@@ -133,6 +133,17 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
     blocks += total;
   }
   __syncthreads();
+  // for the weights: the streams with the longest chunks first, so that the last key tiles drawn are short work
+  if (p.order != nullptr && t < w.n_seqs) {
+    auto length = [&](int s) { return (s + 1 < w.n_seqs ? near_seq[s + 1] : blocks) - near_seq[s]; };
+    const int mine = length(t);
+    int rank = 0;
+    for (int s = 0; s < w.n_seqs; ++s) {
+      const int x = length(s);
+      rank += x > mine || (x == mine && s < t);
+    }
+    p.order[rank] = t;
+  }
   // row ranges that overlap (a start below an earlier one) can ask for more than the rows hold
   if (blocks > p.n_blocks) {
     if (t == 0) paged_report(w, kStatusLength);
@@ -194,6 +205,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
   int rest_tiles;
   const int rest = plan_scan(max(0, n - quota), warp_sums, rest_tiles);
   if (t <= n_tail) out->rest[t] = near_rest[t] = rest;
+  if (t == 0) *p.ticket = 0;
   const int n_ctas = in_step ? kSmCount
                              : static_cast<int>(min(static_cast<long long>(kSmCount), (all + kMinTiles - 1) / kMinTiles));
   if (t == 0) {
@@ -863,12 +875,16 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
 //   allocator and MMA issuer, one S buffer per warpgroup.
 // The exponentials bound it (128 x 128 per tile against 8 MMA steps: 1024 clocks at 16 a clock). Each is
 // one of a chain of short dependent instructions, so two thread blocks per SM take turns, sixteen such
-// warps; and a thread block needs some 10000 clocks besides (start, first tiles, end), which the other covers.
+// warps; and a key tile needs some 6000 clocks besides (K and first query tile, end), which the other covers.
+// The thread blocks stay and draw key tiles from a counter, since their costs differ with the chunks'
+// lengths. (One thread block per key tile of the longest stream: 105 us for four chunks of 128 to 512 tokens over
+// 1024 to 8192, their slots held by empty ones for a third of the time.)
 constexpr int kWGroups = 2;
 constexpr int kWThreads = kWGroups * 128 + 64;
 constexpr int kWSmemQ = kTile;
 constexpr int kWSmemLse = kWSmemQ + kWGroups * kTile;  // [group][2][128] floats: -z per row, two tiles
-constexpr int kWSmemBar = kWSmemLse + kWGroups * 2 * kBM * 4;
+constexpr int kWSmemSum = kWSmemLse + kWGroups * 2 * kBM * 4;  // [group - 1][128]: the other groups' sums
+constexpr int kWSmemBar = kWSmemSum + (kWGroups - 1) * kBM * 4;
 constexpr int kWSmemBytes = kWSmemBar + 256 + 1024;
 
 enum : int {
@@ -881,66 +897,73 @@ enum : int {
   kWbCount
 };
 
+// One query tile's weights of this thread's key, added to acc; rows outside [lo, hi) do not count.
+template <bool kWhole>
+__device__ __forceinline__ void weigh_tile(uint32_t tS, const float* z, uint64_t c2, int lo, int hi, uint64_t* s_empty,
+                                           uint64_t (&acc)[4]) {
+#pragma unroll
+  for (int part = 0; part < 4; ++part) {
+    uint32_t sv[32];
+    ptx::tmem_ld32(tS + part * 32, sv);
+    if (part == 3) {
+      ptx::tc_fence_before();
+      ptx::mbar_arrive(s_empty);
+    }
+    const ulonglong2* zz = reinterpret_cast<const ulonglong2*>(z + part * 32);
+#pragma unroll
+    for (int k = 0; k < 16; k += 2) {
+      const ulonglong2 z2 = zz[k >> 1];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint64_t v = ptx::f2_fma(
+            ptx::f2_pack(__uint_as_float(sv[2 * (k + e)]), __uint_as_float(sv[2 * (k + e) + 1])), c2, e ? z2.y : z2.x);
+        float a, b;
+        ptx::f2_unpack(v, a, b);
+        a = ptx::ex2(a);
+        b = ptx::ex2(b);
+        if (!kWhole) {
+          const int i = part * 32 + 2 * (k + e);
+          a = i >= lo && i < hi ? a : 0.f;
+          b = i + 1 >= lo && i + 1 < hi ? b : 0.f;
+        }
+        acc[(k + e) & 3] = ptx::f2_add(acc[(k + e) & 3], ptx::f2_pack(a, b));
+      }
+    }
+  }
+}
+
 __global__ void __launch_bounds__(kWThreads, 2)
     paged_weight_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ PagedAttnParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* nz = reinterpret_cast<float*>(smem + kWSmemLse);
+  float* sums = reinterpret_cast<float*>(smem + kWSmemSum);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kWSmemBar);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kWbCount);
   const PagedView& w = p.view;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const unsigned long long limit = p.wait_limit_ns;
-  // streams of different chunk lengths side by side in the launch order, so that they share its end
-  const int n_kt = (w.max_kv + kBN - 1) / kBN, n_sh = w.n_seqs * w.kv_heads;
-  const int kt = n_kt - 1 - blockIdx.x / n_sh, sh = blockIdx.x % n_sh;
-  const int h = sh % w.kv_heads, s = sh / w.kv_heads;
+  int* ticket = reinterpret_cast<int*>(bars + kWbCount + 1);
   ptx::let_next_launch();
   ptx::wait_previous();
-  const PagedSeq q = paged_seq(w, s);
-  const int j0 = kt * kBN;
-  if (!q.ok || q.n_q == 0 || j0 >= q.kv) return;  // a bad length was reported by the attention
+  PagedTiles<kBN> place;
+  place.order = p.order;
+  place.count(w, false);  // a bad length was reported by the attention
+  if (static_cast<int>(blockIdx.x) >= place.all) return;
   const int G = p.group;
   const int tpt = kBM / G;
-  const int first_place = q.kv - q.n_q;  // place of the chunk's first token
-  // query tiles from the first with a row that sees this tile's first key
-  const int qt0 = p.causal ? max(0, j0 - first_place) / tpt : 0;
-  const int n_qt = (q.n_q + tpt - 1) / tpt - qt0;
-
-  if (warp == kWGroups * 4) {  // the first loads leave before the rest of the thread block is ready
-    if (lane == 0) {
-      ptx::mbar_init(&bars[kWbK], 1);
-      for (int i = 0; i < kWGroups; ++i) {
-        ptx::mbar_init(&bars[kWbQFull + i], 1);
-        ptx::mbar_init(&bars[kWbQEmpty + i], 1);
-        ptx::mbar_init(&bars[kWbSFull + i], 1);
-        ptx::mbar_init(&bars[kWbSEmpty + i], kBM);
-      }
-      ptx::mbar_init(&bars[kWbDrain], 1);
-      ptx::fence_mbar_init();
+  if (threadIdx.x == 0) {
+    ptx::mbar_init(&bars[kWbK], 1);
+    for (int i = 0; i < kWGroups; ++i) {
+      ptx::mbar_init(&bars[kWbQFull + i], 1);
+      ptx::mbar_init(&bars[kWbQEmpty + i], 1);
+      ptx::mbar_init(&bars[kWbSFull + i], 1);
+      ptx::mbar_init(&bars[kWbSEmpty + i], kBM);
     }
-    __syncwarp();
-    const int box = min(1 << w.page_shift, kBN);
-    const int n_box = kBN / box;
-    const int b = lane % n_box, c = lane / n_box;
-    const int j = j0 + b * box;
-    if (lane == 0) ptx::mbar_arrive_expect_tx(&bars[kWbK], (min(kBN, q.kv - j0) + box - 1) / box * box * 256);
-    __syncwarp();
-    if (c < 2 && j < q.kv)
-      ptx::tma_load_3d(smem + c * kSlab + b * box * 128, &tm_k, &bars[kWbK], c * 64,
-                       (h << w.page_shift) + (j & ((1 << w.page_shift) - 1)),
-                       max(0, paged_id(w, s, j >> w.page_shift)));
+    ptx::mbar_init(&bars[kWbDrain], 1);
+    ptx::fence_mbar_init();
   }
-  auto load_q = [&](int t) {
-    const int st = t % kWGroups;
-    ptx::mbar_arrive_expect_tx(&bars[kWbQFull + st], 2 * 128 * tpt * G);
-    for (int cc = 0; cc < 2; ++cc)
-      ptx::tma_load_3d(smem + kWSmemQ + st * kTile + cc * kSlab, &tm_q, &bars[kWbQFull + st], cc * 64, h * G,
-                       q.q0 + (qt0 + t) * tpt);
-  };
-  if (warp == kWGroups * 4 && lane == 0)
-    for (int t = 0; t < min(n_qt, kWGroups); ++t) load_q(t);
   if (warp == kWGroups * 4 + 1) {
     ptx::tmem_alloc(tmem_slot, kWGroups * 128);
     ptx::tmem_relinquish();
@@ -950,116 +973,132 @@ __global__ void __launch_bounds__(kWThreads, 2)
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp == kWGroups * 4) {
-    if (lane == 0) {
-      bool ok = true;
-      int nq = min(n_qt, kWGroups);
-      for (int t = nq; t < n_qt; ++t) {
-        if (!ptx::mbar_wait(&bars[kWbQEmpty + t % kWGroups], (t / kWGroups - 1) & 1, limit)) { ok = false; break; }
-        load_q(t);
-        nq = t + 1;
-      }
-      if (!ok) paged_report(w, kStatusTimeout);
-      ptx::mbar_wait(&bars[kWbK], 0, kDrainNs);
-      for (int t = max(0, nq - kWGroups); t < nq; ++t)
-        ptx::mbar_wait(&bars[kWbQFull + t % kWGroups], (t / kWGroups) & 1, kDrainNs);
-    }
-    __syncwarp();
-  } else if (warp == kWGroups * 4 + 1) {
-    if (lane == 0) {
-      const uint32_t ka = ptx::smem_u32(smem);
-      bool ok = ptx::mbar_wait(&bars[kWbK], 0, limit);
-      for (int t = 0; ok && t < n_qt; ++t) {
-        const int st = t % kWGroups;  // the query stage, the S buffer and the warpgroup
-        if (!ptx::mbar_wait(&bars[kWbQFull + st], (t / kWGroups) & 1, limit)) { ok = false; break; }
-        if (t >= kWGroups && !ptx::mbar_wait(&bars[kWbSEmpty + st], (t / kWGroups - 1) & 1, limit)) { ok = false; break; }
-        ptx::tc_fence_after();
-        const uint32_t qa = ptx::smem_u32(smem + kWSmemQ + st * kTile);
-#pragma unroll
-        for (int kk = 0; kk < kHeadDim / 16; ++kk)
-          ptx::mma_ss(tmem + st * 128, desc_kmajor(ka, kk), desc_kmajor(qa, kk), kIdescS, kk > 0 ? 1u : 0u);
-        ptx::mma_commit(&bars[kWbSFull + st]);
-        ptx::mma_commit(&bars[kWbQEmpty + st]);
-      }
-      if (!ok) paged_report(w, kStatusTimeout);
-      ptx::mma_commit(&bars[kWbDrain]);
-      ptx::mbar_wait(&bars[kWbDrain], 0, kDrainNs);
-    }
-    __syncwarp();
-  } else {
-    const int wg = warp >> 2;
-    const int r = threadIdx.x & 127;  // key of the tile, and the query row whose z this thread fetches
-    const uint32_t tS = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + wg * 128;
-    const uint64_t c2 = ptx::f2_pack(p.scale_log2, p.scale_log2);
-    const int my_tok = r / G;
-    const float* z_of = p.lse2 + static_cast<long long>(q.q0) * p.q_heads + h * G + r - my_tok * G;
-    // -z of row r of query tile t; what rows of no token get is masked below
-    auto fetch = [&](int t) -> float {
-      const int tok = (qt0 + t) * tpt + my_tok;
-      if (t >= n_qt || my_tok >= tpt || tok >= q.n_q) return 0.f;
-      return -*(z_of + static_cast<long long>(tok) * p.q_heads);
-    };
-    float next = fetch(wg);
-    float* to = p.weight + (static_cast<long long>(s) * w.kv_heads + h) * p.weight_stride + j0 + r;
-    const float old = wg == 0 && j0 + r < first_place ? *to : 0.f;  // the chunk's own keys start from zero
-    uint64_t acc[4] = {0, 0, 0, 0};
-    bool ok = true;
-    int n = 0;  // tiles taken
-    for (int t = wg; t < n_qt; t += kWGroups, ++n) {
-      float* z = nz + (wg * 2 + (n & 1)) * kBM;
-      z[r] = next;
-      next = fetch(t + kWGroups);
-      // rows [lo, hi) of this tile are of the chunk and see this thread's key
-      const int tok0 = (qt0 + t) * tpt;
-      const int hi = min(tpt, q.n_q - tok0) * G;
-      const int lo = p.causal ? max(0, j0 + r - first_place - tok0) * G : 0;
-      const bool whole = __all_sync(0xffffffffu, lo == 0 && hi == kBM);
-      if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars[kWbSFull + wg], n & 1, limit));
-      ptx::named_bar_sync(1 + wg, kBM);  // every row's z is in place; the readers of two tiles ago are past it
-      if (!ok) continue;
-      ptx::tc_fence_after();
-#pragma unroll
-      for (int part = 0; part < 4; ++part) {
-        uint32_t sv[32];
-        ptx::tmem_ld32(tS + part * 32, sv);
-        if (part == 3) {
-          ptx::tc_fence_before();
-          ptx::mbar_arrive(&bars[kWbSEmpty + wg]);
-        }
-        const ulonglong2* zz = reinterpret_cast<const ulonglong2*>(z + part * 32);
-#pragma unroll
-        for (int k = 0; k < 16; k += 2) {
-          const ulonglong2 z2 = zz[k >> 1];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const uint64_t x = ptx::f2_fma(
-                ptx::f2_pack(__uint_as_float(sv[2 * (k + e)]), __uint_as_float(sv[2 * (k + e) + 1])), c2, e ? z2.y : z2.x);
-            float a, b;
-            ptx::f2_unpack(x, a, b);
-            a = ptx::ex2(a);
-            b = ptx::ex2(b);
-            if (!whole) {
-              const int i = part * 32 + 2 * (k + e);
-              a = i >= lo && i < hi ? a : 0.f;
-              b = i + 1 >= lo && i + 1 < hi ? b : 0.f;
-            }
-            acc[(k + e) & 3] = ptx::f2_add(acc[(k + e) & 3], ptx::f2_pack(a, b));
-          }
-        }
-      }
-    }
-    if (!ok && lane == 0) paged_report(w, kStatusTimeout);
-    // the warpgroups' sums of a key, in order
-    ptx::named_bar_sync(1 + kWGroups, kWGroups * kBM);  // every z was read
-    nz[wg * kBM + r] = sum_of(acc);
-    ptx::named_bar_sync(1 + kWGroups, kWGroups * kBM);
-    if (wg == 0 && ok && j0 + r < q.kv) {
-      float sum = nz[r];
-      for (int g = 1; g < kWGroups; ++g) sum += nz[g * kBM + r];
-      *to = old + sum;
-    }
-  }
+  long long x = blockIdx.x;  // this thread block's unit; the next one is drawn while it is worked on
+  int n_k = 0, g0 = 0;       // units with work done, and their query tiles
+  bool ok = true;            // no wait of this thread's warp has expired
+  while (x < place.all) {
+    unsigned drawn = 0;
+    if (threadIdx.x == 0) drawn = atomicAdd(p.ticket, 1u);
+    place.go_to(w, x);
+    const PagedSeq& q = place.q;
+    const int s = place.s, h = place.h, j0 = place.t * kBN;
+    const int first_place = q.kv - q.n_q;  // place of the chunk's first token
+    // query tiles from the first with a row that sees this tile's first key (none if nothing is cached)
+    const int qt0 = p.causal ? max(0, j0 - first_place) / tpt : 0;
+    const int n_qt = j0 < q.kv ? (q.n_q + tpt - 1) / tpt - qt0 : 0;
 
+    if (warp == kWGroups * 4) {
+      // ---------------------------------------------------------- TMA producer
+      const int box = min(1 << w.page_shift, kBN);
+      const int n_box = kBN / box;
+      const int b = lane % n_box, c = lane / n_box;
+      const int j = j0 + b * box;
+      if (n_qt > 0) {
+        if (lane == 0) ptx::mbar_arrive_expect_tx(&bars[kWbK], (min(kBN, q.kv - j0) + box - 1) / box * box * 256);
+        __syncwarp();
+        if (c < 2 && j < q.kv)
+          ptx::tma_load_3d(smem + c * kSlab + b * box * 128, &tm_k, &bars[kWbK], c * 64,
+                           (h << w.page_shift) + (j & ((1 << w.page_shift) - 1)),
+                           max(0, paged_id(w, s, j >> w.page_shift)));
+        __syncwarp();
+        if (lane == 0) {
+          for (int t = 0; ok && t < n_qt; ++t) {
+            const int g = g0 + t, st = g % kWGroups;
+            if (g >= kWGroups) ok = ptx::mbar_wait(&bars[kWbQEmpty + st], (g / kWGroups - 1) & 1, limit);
+            if (!ok) break;
+            ptx::mbar_arrive_expect_tx(&bars[kWbQFull + st], 2 * 128 * tpt * G);
+            for (int cc = 0; cc < 2; ++cc)
+              ptx::tma_load_3d(smem + kWSmemQ + st * kTile + cc * kSlab, &tm_q, &bars[kWbQFull + st], cc * 64, h * G,
+                               q.q0 + (qt0 + t) * tpt);
+          }
+          // every copy issued lands before the K tile's memory, or the thread block, is given up
+          ptx::mbar_wait(&bars[kWbK], n_k & 1, kDrainNs);
+        }
+      }
+      __syncwarp();
+    } else if (warp == kWGroups * 4 + 1) {
+      // ---------------------------------------------------------- MMA issuer
+      if (lane == 0 && n_qt > 0) {
+        const uint32_t ka = ptx::smem_u32(smem);
+        if (ok) ok = ptx::mbar_wait(&bars[kWbK], n_k & 1, limit);
+        for (int t = 0; ok && t < n_qt; ++t) {
+          const int g = g0 + t, st = g % kWGroups;  // the query stage, the S buffer and the warpgroup
+          ok = ptx::mbar_wait(&bars[kWbQFull + st], (g / kWGroups) & 1, limit) &&
+               (g < kWGroups || ptx::mbar_wait(&bars[kWbSEmpty + st], (g / kWGroups - 1) & 1, limit));
+          if (!ok) break;
+          ptx::tc_fence_after();
+          const uint32_t qa = ptx::smem_u32(smem + kWSmemQ + st * kTile);
+#pragma unroll
+          for (int kk = 0; kk < kHeadDim / 16; ++kk)
+            ptx::mma_ss(tmem + st * 128, desc_kmajor(ka, kk), desc_kmajor(qa, kk), kIdescS, kk > 0 ? 1u : 0u);
+          ptx::mma_commit(&bars[kWbSFull + st]);
+          ptx::mma_commit(&bars[kWbQEmpty + st]);
+        }
+      }
+      __syncwarp();
+    } else if (n_qt > 0) {
+      const int wg = warp >> 2;
+      const int r = threadIdx.x & 127;  // key of the tile, and the query row whose z this thread fetches
+      const uint32_t tS = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + wg * 128;
+      const uint64_t c2 = ptx::f2_pack(p.scale_log2, p.scale_log2);
+      const int my_tok = r / G;
+      const float* z_of = p.lse2 + static_cast<long long>(q.q0) * p.q_heads + h * G + r - my_tok * G;
+      // -z of row r of query tile t; what rows of no token get is masked below
+      auto fetch = [&](int t) -> float {
+        const int tok = (qt0 + t) * tpt + my_tok;
+        if (t >= n_qt || my_tok >= tpt || tok >= q.n_q) return 0.f;
+        return -*(z_of + static_cast<long long>(tok) * p.q_heads);
+      };
+      const int t0 = (wg - g0) & (kWGroups - 1);  // this warpgroup's first tile of the unit
+      float next = fetch(t0);
+      float* to = p.weight + (static_cast<long long>(s) * w.kv_heads + h) * p.weight_stride + j0 + r;
+      const float old = wg == 0 && j0 + r < first_place ? *to : 0.f;  // the chunk's own keys start from zero
+      uint64_t acc[4] = {0, 0, 0, 0};
+      for (int t = t0; t < n_qt; t += kWGroups) {
+        const int n = (g0 + t) / kWGroups;  // tiles that this warpgroup took before
+        float* z = nz + (wg * 2 + (n & 1)) * kBM;
+        z[r] = next;
+        next = fetch(t + kWGroups);
+        // rows [lo, hi) of this tile are of the chunk and see this thread's key
+        const int tok0 = (qt0 + t) * tpt;
+        const int hi = min(tpt, q.n_q - tok0) * G;
+        const int lo = p.causal ? max(0, j0 + r - first_place - tok0) * G : 0;
+        const bool whole = __all_sync(0xffffffffu, lo == 0 && hi == kBM);
+        if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars[kWbSFull + wg], n & 1, limit));
+        ptx::named_bar_sync(1 + wg, kBM);  // every row's z is in place; the readers of two tiles ago are past it
+        if (!ok) continue;
+        ptx::tc_fence_after();
+        // two copies, so that whole tiles pay nothing for the mask (its compares and selects were three
+        // fifths of all instructions)
+        if (whole)
+          weigh_tile<true>(tS, z, c2, lo, hi, &bars[kWbSEmpty + wg], acc);
+        else
+          weigh_tile<false>(tS, z, c2, lo, hi, &bars[kWbSEmpty + wg], acc);
+      }
+      // the warpgroups' sums of a key, in order
+      if (wg != 0) sums[(wg - 1) * kBM + r] = sum_of(acc);
+      ptx::named_bar_sync(1 + kWGroups, kWGroups * kBM);
+      if (wg == 0 && ok && j0 + r < q.kv) {
+        float sum = sum_of(acc);
+        for (int i = 0; i < kWGroups - 1; ++i) sum += sums[i * kBM + r];
+        *to = old + sum;
+      }
+    }
+    g0 += n_qt;
+    n_k += n_qt > 0;
+    if (threadIdx.x == 0) *ticket = static_cast<int>(min(drawn, 0x7fffffffu - gridDim.x));
+    __syncthreads();
+    x = static_cast<long long>(gridDim.x) + *ticket;
+    __syncthreads();
+  }
+  if (!ok && lane == 0) paged_report(w, kStatusTimeout);
+  if (warp == kWGroups * 4 && lane == 0)  // the last query tiles' copies
+    for (int g = max(0, g0 - kWGroups); g < g0; ++g) ptx::mbar_wait(&bars[kWbQFull + g % kWGroups], (g / kWGroups) & 1, kDrainNs);
+  if (warp == kWGroups * 4 + 1 && lane == 0) {
+    // everything issued must complete before TMEM is released
+    ptx::mma_commit(&bars[kWbDrain]);
+    ptx::mbar_wait(&bars[kWbDrain], 0, kDrainNs);
+  }
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
@@ -1102,9 +1141,7 @@ cudaError_t launch_paged_weight(const CUtensorMap& tm_q, const CUtensorMap& tm_k
                                 cudaStream_t stream) {
   const cudaError_t err = configure();
   if (err != cudaSuccess) return err;
-  const unsigned n_kt = (p.view.max_kv + kBN - 1) / kBN;
-  const unsigned grid = n_kt * p.view.n_seqs * p.view.kv_heads;
-  return launch_after(paged_weight_kernel, grid, kWThreads, kWSmemBytes, stream, tm_q, tm_k, p);
+  return launch_after(paged_weight_kernel, 2 * kSmCount, kWThreads, kWSmemBytes, stream, tm_q, tm_k, p);
 }
 
 }  // namespace rkv

@@ -48,11 +48,6 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// Tiles of one KV head of a stream: none without rows, one (all masked) if nothing is cached.
-__device__ __forceinline__ int seq_tiles(const PagedSeq& q) {
-  return q.ok && q.n_q > 0 ? max(1, (q.kv + kTileKeys - 1) / kTileKeys) : 0;
-}
-
 // A unit, or the part of one, of a thread block's share.
 struct TokenUnit {
   PagedSeq q;
@@ -60,77 +55,19 @@ struct TokenUnit {
   int t0, t1, tiles;  // its tiles, and the unit's
 };
 
-// x / y where both nearly always fit 32 bits (a 64-bit division is some 100 instructions).
-__device__ __forceinline__ long long quotient(long long x, int y) {
-  return (x >> 32) == 0 ? static_cast<long long>(static_cast<unsigned>(x) / static_cast<unsigned>(y)) : x / y;
-}
-
-// All tiles of the batch, and a place among them. Whole warps call these.
-struct TokenWalk {
-  long long each, left;  // tiles of a share (the first `more` shares have one more), tiles still to walk
+// The shares of all units' tiles, and one thread block's way through its own. Whole warps call these.
+struct TokenWalk : PagedTiles<kTileKeys> {
+  long long left;        // tiles still to walk
+  long long each;        // tiles of a share; the first `more` shares have one more
   int n, more;           // shares
-  int s, h, t;           // the place: stream, head, tile
-  PagedSeq q;
-  int tiles;
-  int q0, n_q, kv, mine;  // lane l: stream l of the first 32, and its tiles of one head
 
-  __device__ __forceinline__ void count(const PagedView& w) {
-    const int lane = threadIdx.x & 31;
-    long long all = 0;
-    for (int base = 0; base < w.n_seqs; base += 32) {
-      int x = 0;
-      if (base + lane < w.n_seqs) {
-        const PagedSeq y = paged_seq(w, base + lane);
-        if (!y.ok && blockIdx.x == 0) paged_report(w, kStatusLength);
-        x = seq_tiles(y);
-        if (base == 0) {
-          q0 = y.q0;
-          n_q = y.n_q;
-          kv = y.kv;
-        }
-      }
-      if (base == 0) mine = x;
-      all += __reduce_add_sync(0xffffffffu, x);
-    }
-    all *= w.kv_heads;
+  __device__ __forceinline__ void share(const PagedView& w) {
+    count(w, blockIdx.x == 0);
     n = static_cast<int>(min(static_cast<long long>(2 * kSmCount), (all + kMinTiles - 1) / kMinTiles));
     each = n > 0 ? quotient(all, n) : 0;
     more = static_cast<int>(all - each * n);
   }
   __device__ __forceinline__ long long start(int c) const { return each * c + min(c, more); }
-  __device__ __forceinline__ void go_to(const PagedView& w, long long x) {
-    const int lane = threadIdx.x & 31;
-    long long before = 0;
-    for (int base = 0; base < w.n_seqs; base += 32) {
-      const int c = base == 0 ? mine : base + lane < w.n_seqs ? seq_tiles(paged_seq(w, base + lane)) : 0;
-      int inc = c;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, inc, d);
-        if (lane >= d) inc += y;
-      }
-      const unsigned hit = __ballot_sync(0xffffffffu, (before + inc) * w.kv_heads > x);
-      if (hit) {
-        const int l = __ffs(hit) - 1;
-        s = base + l;
-        before += __shfl_sync(0xffffffffu, inc - c, l);
-        tiles = __shfl_sync(0xffffffffu, c, l);
-        if (base == 0) {
-          q.q0 = __shfl_sync(0xffffffffu, q0, l);
-          q.n_q = __shfl_sync(0xffffffffu, n_q, l);
-          q.kv = __shfl_sync(0xffffffffu, kv, l);
-          q.ok = true;
-        } else {
-          q = paged_seq(w, s);
-        }
-        break;
-      }
-      before += __shfl_sync(0xffffffffu, inc, 31);
-    }
-    const long long in = x - before * w.kv_heads;
-    h = static_cast<int>(quotient(in, tiles));
-    t = static_cast<int>(in - static_cast<long long>(h) * tiles);
-  }
   // What the join has to do where share c starts: nothing unless this is the first border inside a unit.
   __device__ __forceinline__ PagedCut cut(int c) const {
     PagedCut r = {};
@@ -157,7 +94,7 @@ struct TokenWalk {
       h = 0;
       do {
         q = paged_seq(w, ++s);
-        tiles = seq_tiles(q);
+        tiles = paged_seq_tiles<kTileKeys>(q);
       } while (tiles == 0);
     }
     return true;
@@ -501,8 +438,9 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
     ptx::fence_mbar_init();
   }
   ptx::wait_previous();
+  if (cta == 0 && threadIdx.x == 0) *p.ticket = 0;
   TokenWalk walk;
-  walk.count(w);
+  walk.share(w);
   if (cta >= walk.n) {
     if (threadIdx.x == 0) p.cuts[cta] = PagedCut{};
     return;

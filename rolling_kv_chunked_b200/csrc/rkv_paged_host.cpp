@@ -113,16 +113,18 @@ rkv::PagedPlan plan_of(const rkv_page_pool* pool, const rkv_paged_batch* b, int 
     return at;
   };
   p.lse = weight ? take(4 * heads) : -1;
-  p.cuts = p.blocks = p.work = p.seq_first = -1;
+  p.cuts = p.blocks = p.work = p.seq_first = p.order = -1;
   const long long rows = p.slot_rows ? 4LL * rkv::kSmCount * p.slot_rows : 2LL * rkv::kSmCount * rkv::kPagedPartRows;
   p.part = take(4 * rows * kHeadDim);
   p.part_ml = take(8 * rows);
+  p.ticket = take(4);
   if (p.slot_rows) {
     p.cuts = take(2LL * rkv::kSmCount * sizeof(rkv::PagedCut));
   } else {
     p.blocks = take(static_cast<long long>(sizeof(rkv::PagedBlock)) * p.n_blocks);
     p.work = take(sizeof(rkv::PagedWork));
     p.seq_first = take(4LL * b->n_seqs);
+    if (weight && b->n_seqs <= rkv::kPagedMaxOrder) p.order = take(4LL * b->n_seqs);
   }
   p.score_stride = (b->max_kv + 63LL) / 64 * 64;
   // scores are kept for at most 16 rows: 8 bytes of traffic for each, where reading K again takes 256
@@ -212,13 +214,15 @@ RKV_API int rkv_paged_attention(const rkv_page_pool* pool, const rkv_paged_batch
   p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(kHeadDim)));
   char* ws = static_cast<char*>(workspace);
   if (plan.lse >= 0) p.lse2 = reinterpret_cast<float*>(ws + plan.lse);
-  if (plan.part >= 0) p.part = reinterpret_cast<float*>(ws + plan.part);
-  if (plan.part_ml >= 0) p.part_ml = reinterpret_cast<float2*>(ws + plan.part_ml);
+  p.part = reinterpret_cast<float*>(ws + plan.part);
+  p.part_ml = reinterpret_cast<float2*>(ws + plan.part_ml);
+  p.ticket = reinterpret_cast<unsigned*>(ws + plan.ticket);
   if (plan.cuts >= 0) p.cuts = reinterpret_cast<rkv::PagedCut*>(ws + plan.cuts);
   if (plan.blocks >= 0) {
     p.blocks = reinterpret_cast<rkv::PagedBlock*>(ws + plan.blocks);
     p.work = reinterpret_cast<rkv::PagedWork*>(ws + plan.work);
     p.seq_first = reinterpret_cast<int*>(ws + plan.seq_first);
+    if (plan.order >= 0) p.order = reinterpret_cast<int*>(ws + plan.order);
   }
   if (plan.scores >= 0) p.scores = reinterpret_cast<float*>(ws + plan.scores);
   p.score_stride = plan.score_stride;
