@@ -1,6 +1,6 @@
-// Pieces shared by the attention kernels on tcgen05: 128 x 128 bf16 tiles in shared memory (two
-// 64-column halves, 128-byte swizzle), their matrix descriptors, and a query row's accumulator in
-// TMEM.
+// Pieces of the paged caches' tcgen05 kernels: 128 x 128 bf16 tiles in shared memory (two 64-column
+// halves, 128-byte swizzle), their matrix descriptors, and a query row's accumulator in TMEM: the tile
+// layout of the rolling-window kernel (rkv_attention.cu).
 #pragma once
 
 #include "numeric.cuh"

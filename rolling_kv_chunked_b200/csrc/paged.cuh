@@ -4,7 +4,7 @@
 
 #include <utility>
 
-#include "rkv_internal.h"
+#include "paged_internal.h"
 
 namespace rkv {
 

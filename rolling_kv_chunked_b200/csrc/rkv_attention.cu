@@ -50,7 +50,6 @@
 #include <cfloat>
 #include <mutex>
 
-#include "attention_tile.cuh"
 #include "numeric.cuh"
 #include "ptx_sm100.cuh"
 #include "rkv_internal.h"
@@ -60,6 +59,8 @@ namespace {
 
 constexpr int kBM = 128;                  // query rows per tile (TMEM lanes)
 constexpr int kBN = 128;                  // keys per tile
+constexpr int kSlab = 128 * 64 * 2;       // 128 rows x 64 bf16, one 128-byte swizzle span per row
+constexpr int kTile = 2 * kSlab;          // 128 rows x 128 bf16
 constexpr int kThreads = 320;
 constexpr int kSmemQ = 0;                 // Q0, Q1
 constexpr int kSmemK = 2 * kTile;         // K stage 0, 1
@@ -110,6 +111,23 @@ __device__ __forceinline__ void tile_of(const AttnParams& p, int j, int& src, in
   src = 0;
   krow = vrow = 0;
   valid = 0;
+}
+
+// K-major operand (Q or K tile): k-step kk covers elements [16kk, 16kk+16) of every row.
+__device__ __forceinline__ uint64_t desc_kmajor(uint32_t tile_addr, int kk) {
+  return ptx::smem_desc_sw128(tile_addr + (kk >> 2) * kSlab + (kk & 3) * 32, 16, 1024);
+}
+
+// MN-major operand (V tile as B of O += P V): k-step kk covers keys [16kk, 16kk+16);
+// the two 64-column halves of d are kSlab apart.
+__device__ __forceinline__ uint64_t desc_v(uint32_t tile_addr, int kk) {
+  return ptx::smem_desc_sw128(tile_addr + kk * 2048, kSlab, 1024);
+}
+
+// two fp32 -> packed bf16x2 (lo in the low half), round to nearest even, one conversion
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
 }
 
 // 2^x for two lanes on the FMA / integer pipes instead of the special-function unit:
@@ -190,6 +208,24 @@ __device__ __forceinline__ void numerators_half(const uint32_t* sh, uint64_t c2,
     }
     acc[k & 3] = ptx::f2_add(acc[k & 3], ptx::f2_pack(a, b));
     pk[k] = pack_bf16x2(a, b);
+  }
+}
+
+__device__ __forceinline__ float lg2_approx(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// O (this thread's row, 128 fp32 TMEM columns at tO) *= f
+__device__ __forceinline__ void scale_o(uint32_t tO, float f) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    uint32_t rr[32];
+    ptx::tmem_ld32(tO + 32 * c, rr);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) rr[i] = __float_as_uint(__uint_as_float(rr[i]) * f);
+    ptx::tmem_st32(tO + 32 * c, rr);
   }
 }
 

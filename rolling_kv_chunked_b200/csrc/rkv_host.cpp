@@ -23,6 +23,7 @@
 
 #include "../../include/rkv.h"
 #include "rkv_internal.h"
+#include "tensor_map.h"
 
 #define RKV_API extern "C" __attribute__((visibility("default")))
 

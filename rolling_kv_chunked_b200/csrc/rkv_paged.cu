@@ -4,7 +4,7 @@
 #include <mutex>
 
 #include "paged.cuh"
-#include "ptx_sm100.cuh"
+#include "ptx_warp.cuh"
 
 namespace rkv {
 namespace {

@@ -31,6 +31,7 @@
 
 #include "attention_tile.cuh"
 #include "paged.cuh"
+#include "ptx_warp.cuh"
 
 namespace rkv {
 namespace {

@@ -21,7 +21,7 @@
 
 #include "numeric.cuh"
 #include "paged.cuh"
-#include "ptx_sm100.cuh"
+#include "ptx_warp.cuh"
 
 namespace rkv {
 namespace {

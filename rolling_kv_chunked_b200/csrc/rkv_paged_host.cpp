@@ -6,7 +6,7 @@
 #include <cstring>
 
 #include "../../include/rkv.h"
-#include "rkv_internal.h"
+#include "paged_internal.h"
 
 #define RKV_API extern "C" __attribute__((visibility("default")))
 
