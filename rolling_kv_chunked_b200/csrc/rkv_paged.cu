@@ -1,6 +1,7 @@
 // The paged cache's data movement: the write of a chunk into pages and eviction by weight.
 #include <cooperative_groups.h>
 
+#include <algorithm>
 #include <mutex>
 
 #include "paged.cuh"
@@ -76,23 +77,25 @@ __device__ __forceinline__ unsigned weight_key(float x) {
 // Measured, one stream of 65536 tokens and eight heads: 154 us with one block per head; in cycles of the
 // cluster form, per digit: counting 1000, the barrier 1650, the histograms 2100 (16 bytes a clock through
 // distributed shared memory: the held form therefore packs two counts to a word), finding 600.
-constexpr int kSelThreads = 1024;
-constexpr int kSelWarps = kSelThreads / 32;
+// Blocks have 1024 threads; many heads of short streams (to 4096 tokens) take 256, eight to an SM.
 constexpr int kSelCluster = 8;  // blocks of a cluster at most
 constexpr int kHeldKeys = 16;
+constexpr int kDigits = 2048;
 
 // kHeld: every warp's run has at most 32 * kHeldKeys tokens, a block's then less than 65536.
-template <bool kHeld>
+template <int kSelThreads, bool kHeld>
 __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(const __grid_constant__ PagedEvictParams p) {
   namespace cg = cooperative_groups;
   cg::cluster_group cluster = cg::this_cluster();
-  // counts of 2048 digits, by pass (a neighbour may still read the last pass's): two digits to a word if
-  // held, else one; thread t looks at the pair of digits 2t, 2t + 1
-  constexpr int kWords = kHeld ? 1 : 2;
-  struct __align__(4 * kWords) Pair {
+  // counts of the digits, by pass (a neighbour may still read the last pass's): two digits to a word if held,
+  // else one; a thread looks at kOwn of them in a row
+  constexpr int kSelWarps = kSelThreads / 32;
+  constexpr int kOwn = kDigits / kSelThreads;
+  constexpr int kWords = kHeld ? kOwn / 2 : kOwn;
+  struct __align__(4 * kWords) Own {
     unsigned x[kWords];
   };
-  __shared__ Pair hist[3][kSelThreads];
+  __shared__ Own hist[3][kSelThreads];
   __shared__ int warp_sums[kSelWarps];
   __shared__ int found[2];
   __shared__ int2 counts[kSelWarps];  // kept above the rank's weight (or fixed), and its equals, by warp
@@ -160,21 +163,24 @@ __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(const __grid_
         }
       });
       cluster.sync();
-      // thread t owns two digits, from the top: 2 (1023 - t) and the one above
-      const int q = kSelThreads - 1 - static_cast<int>(threadIdx.x);
-      Pair part[kSelCluster];
+      // thread t's digits, counted from the top: kOwn (kSelThreads - 1 - t) and those above it
+      const int own = kSelThreads - 1 - static_cast<int>(threadIdx.x);
+      Own part[kSelCluster];
 #pragma unroll
       for (int r = 0; r < kSelCluster; ++r)  // all on their way at once; a smaller cluster reads some twice
-        part[r] = cluster.map_shared_rank(hist[pass], min(r, size - 1))[q];
-      int lo = 0, hi = 0;
+        part[r] = cluster.map_shared_rank(hist[pass], min(r, size - 1))[own];
+      int bins[kOwn], sum = 0;
 #pragma unroll
-      for (int r = 0; r < kSelCluster; ++r) {
-        const unsigned l = kHeld ? part[r].x[0] & 0xffffu : part[r].x[0];
-        const unsigned h = kHeld ? part[r].x[0] >> 16 : part[r].x[kWords - 1];
-        lo += r < size ? static_cast<int>(l) : 0;
-        hi += r < size ? static_cast<int>(h) : 0;
+      for (int i = 0; i < kOwn; ++i) {
+        bins[i] = 0;
+#pragma unroll
+        for (int r = 0; r < kSelCluster; ++r) {
+          const unsigned v = kHeld ? (i & 1 ? part[r].x[i / 2] >> 16 : part[r].x[i / 2] & 0xffffu) : part[r].x[i % kWords];
+          bins[i] += r < size ? static_cast<int>(v) : 0;
+        }
+        sum += bins[i];
       }
-      int inc = lo + hi;
+      int inc = sum;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, inc, d);
@@ -182,13 +188,14 @@ __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(const __grid_
       }
       if (lane == 31) warp_sums[warp] = inc;
       __syncthreads();
-      const int above = inc - lo - hi + __reduce_add_sync(0xffffffffu, lane < warp ? warp_sums[lane] : 0);
-      if (above < rem && rem <= above + hi) {
-        found[0] = 2 * q + 1;
-        found[1] = rem - above;
-      } else if (above + hi < rem && rem <= above + hi + lo) {
-        found[0] = 2 * q;
-        found[1] = rem - above - hi;
+      int above = inc - sum + __reduce_add_sync(0xffffffffu, lane < warp ? warp_sums[lane] : 0);
+#pragma unroll
+      for (int i = kOwn - 1; i >= 0; --i) {
+        if (above < rem && rem <= above + bins[i]) {
+          found[0] = kOwn * own + i;
+          found[1] = rem - above;
+        }
+        above += bins[i];
       }
       __syncthreads();
       prefix |= static_cast<unsigned>(found[0]) << shift;
@@ -213,7 +220,7 @@ __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(const __grid_
   n_tie = __reduce_add_sync(0xffffffffu, n_tie);
   if (lane == 0) counts[warp] = make_int2(n_take, n_tie);
   __syncthreads();
-  const int2 mine = counts[lane];
+  const int2 mine = lane < kSelWarps ? counts[lane] : make_int2(0, 0);
   int2 before;
   before.x = __reduce_add_sync(0xffffffffu, lane < warp ? mine.x : 0);
   before.y = __reduce_add_sync(0xffffffffu, lane < warp ? mine.y : 0);
@@ -437,13 +444,15 @@ cudaError_t launch_paged_write(const PagedWriteParams& p, cudaStream_t stream) {
 
 cudaError_t launch_paged_evict(const PagedEvictParams& p, cudaStream_t stream) {
   const unsigned heads = static_cast<unsigned>(p.view.n_seqs) * p.view.kv_heads;
-  // blocks per cluster: as many as keep one block to an SM, each with at least 2048 tokens of the
-  // longest stream
-  constexpr unsigned kPlaces = 148;
+  // Blocks per cluster: as many as keep one block of 1024 threads to an SM, each with at least 2048 tokens of the
+  // longest stream. Where one block already has less than that and there are more heads than SMs, 256 threads
+  // (440 heads of 556 tokens: 17 us with 1024, three waves).
+  const bool small = heads > kSmCount && p.view.max_kv <= 256 * kHeldKeys;
   unsigned size = kSelCluster;
-  while (size > 1 && (heads * size > kPlaces || static_cast<unsigned>(p.view.max_kv) < 2048u * size)) size /= 2;
-  const long long run = (p.view.max_kv + static_cast<long long>(size) * kSelWarps - 1) / (size * kSelWarps);
-  const bool held = run <= 32 * kHeldKeys;
+  while (size > 1 && (heads * size > kSmCount || static_cast<unsigned>(p.view.max_kv) < 2048u * size)) size /= 2;
+  const int threads = small ? 256 : 1024;
+  const long long piece = static_cast<long long>(size) * (threads / 32);
+  const bool held = (p.view.max_kv + piece - 1) / piece <= 32 * kHeldKeys;
   cudaError_t err = configure();
   if (err != cudaSuccess) return err;
   cudaLaunchAttribute attr[2];
@@ -454,12 +463,12 @@ cudaError_t launch_paged_evict(const PagedEvictParams& p, cudaStream_t stream) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(heads * size);
-  cfg.blockDim = dim3(kSelThreads);
+  cfg.blockDim = dim3(threads);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  err = held ? cudaLaunchKernelEx(&cfg, paged_select_kernel<true>, p)
-             : cudaLaunchKernelEx(&cfg, paged_select_kernel<false>, p);
+  err = cudaLaunchKernelEx(&cfg, small ? paged_select_kernel<256, true> : held ? paged_select_kernel<1024, true>
+                                                                               : paged_select_kernel<1024, false>, p);
   if (err != cudaSuccess) return err;
   // blocks that share a column: up to eight, while the grid stays near three blocks to an SM
   size = kMoveCluster;
@@ -467,7 +476,9 @@ cudaError_t launch_paged_evict(const PagedEvictParams& p, cudaStream_t stream) {
   attr[0].val.clusterDim.x = size;
   cfg.gridDim = dim3(heads * (2 * kMoveParts + 1) * size);
   cfg.blockDim = dim3(kMoveThreads);
-  cfg.dynamicSmemBytes = kMoveSmem;
+  // no more tiles in shared memory than the longest list has
+  const long long tiles = (p.keep + static_cast<long long>(size) * kMoveTokens * kMoveSteps - 1) / (size * kMoveTokens * kMoveSteps);
+  cfg.dynamicSmemBytes = static_cast<size_t>(std::min<long long>(tiles, kMoveAhead + 1)) * kMoveSteps * kMoveThreads * 16;
   return cudaLaunchKernelEx(&cfg, paged_move_kernel, p);
 }
 

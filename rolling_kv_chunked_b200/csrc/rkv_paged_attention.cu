@@ -74,7 +74,8 @@ constexpr uint32_t kIdescPV = ptx::idesc_bf16_f32(kBM, kHeadDim, true);
 
 // ---------------------------------------------------------------- the plan
 constexpr int kPlanThreads = 1024;
-constexpr int kMinTiles = 4;  // key tiles of a thread block's share at least
+constexpr int kMinTiles = 1;  // key tiles of a thread block's share at least: idle SMs cost more than the merge (6 units of 8 to
+                              // 11 tiles: 25 us with 4, 16 with 1)
 
 // Exclusive sum over the thread block, and its total.
 __device__ __forceinline__ int plan_scan(int x, int* warp_sums, int& total) {
@@ -208,7 +209,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
   if (t <= n_tail) out->rest[t] = near_rest[t] = rest;
   if (t == 0) *p.ticket = 0;
   const int n_ctas = in_step ? kSmCount
-                             : static_cast<int>(min(static_cast<long long>(kSmCount), (all + kMinTiles - 1) / kMinTiles));
+                             : static_cast<int>(min(static_cast<long long>(kSmCount), max(units, (all + kMinTiles - 1) / kMinTiles)));
   if (t == 0) {
     out->n_blocks = blocks;
     out->n_ctas = n_ctas;
