@@ -246,6 +246,36 @@ def test_many_streams():
     assert c.batch.poll() == rkv.OK
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("kvs,qs,hq,hk,page", [
+    ([1400], [1100], 40, 40, 16),                # 200 equal units on 148 SMs: a whole wave, and 52 shared in step
+    ([700, 690, 710], [260, 250, 256], 16, 16, 64),  # 96 units of nearly one size, none whole: all shared in step
+    ([1500, 60, 900, 10, 333], [700, 60, 40, 10, 200], 24, 8, 32),  # shared in a row, cut anywhere
+    ([5000], [130], 2, 2, 128),                  # two units, 40 tiles each, over 80 thread blocks
+    ([300] * 20, [32] * 20, 20, 20, 16),         # 32 rows: the last of the single-token form
+    ([300] * 20, [33] * 20, 20, 20, 16),         # 33: the first of the chunk form
+    ([260, 90, 33, 16, 400], [16, 1, 8, 2, 4], 8, 4, 16),  # 32 rows and fewer in one batch
+])
+def test_shared_work(kvs, qs, hq, hk, page, causal):
+    c = Cache(31, kvs, qs, hq, hk, page)
+    old = torch.rand((len(kvs), hk, c.max_kv), device="cuda")
+    weight = old.clone()
+    out, z = c.attend(causal, weight=weight)
+    c.check(out, z, causal, weight, old)
+
+
+def test_many_streams_with_chunks():
+    """More streams, and more blocks of rows, than the plan holds in shared memory."""
+    n = 1100
+    kvs = [(i * 37) % 120 for i in range(n)]
+    qs = [min(k, (i * 7) % 60) for i, k in enumerate(kvs)]
+    c = Cache(32, kvs, qs, 2, 2, 16)
+    old = torch.rand((n, 2, c.max_kv), device="cuda")
+    weight = old.clone()
+    out, z = c.attend(weight=weight)
+    c.check(out, z, True, weight, old)
+
+
 @pytest.mark.parametrize("kvs,qs,hk,page", [([1], [1], 1, 16), ([33, 0, 16, 500], [1, 0, 16, 200], 3, 16),
                                             ([129, 128], [129, 1], 8, 128), ([70, 200], [7, 130], 40, 64)])
 def test_write(kvs, qs, hk, page):
@@ -321,11 +351,21 @@ def test_evict_among_equals_and_odd_weights(kind):
     _evict_and_check(c, weight, 600, 7, 33)
 
 
-@pytest.mark.parametrize("page", [16, 128])
-def test_evict_a_long_stream(page):
-    c = Cache(21, [70001], [0], 2, 2, page)
-    weight = torch.rand((1, 2, 70001), generator=c.g, device="cuda") ** 8
-    _evict_and_check(c, weight, 20011, 64, 1000)
+@pytest.mark.parametrize("page,n,keep", [(16, 70001, 20011), (128, 70001, 20011), (128, 140001, 70000)])
+def test_evict_a_long_stream(page, n, keep):
+    c = Cache(21, [n], [0], 2, 2, page)
+    weight = torch.rand((1, 2, n), generator=c.g, device="cuda") ** 8
+    _evict_and_check(c, weight, keep, 64, 1000)
+
+
+@pytest.mark.parametrize("max_kv", [700, 4097])
+def test_evict_many_heads(max_kv):
+    """More heads than SMs, short streams and streams that may be longer."""
+    n = 40
+    c = Cache(30, [(i * 97) % 700 + 1 for i in range(n)], [0] * n, 4, 4, 16, max_kv=max_kv)
+    weight = torch.rand((n, 4, max_kv), generator=c.g, device="cuda") ** 3
+    weight[:, 1] = (weight[:, 1] * 2).round()
+    _evict_and_check(c, weight, 150, 3, 40)
 
 
 @pytest.mark.parametrize("qs", [1, 6, 150])
