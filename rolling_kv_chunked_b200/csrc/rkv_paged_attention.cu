@@ -368,7 +368,7 @@ struct PagedWalk {
 // 64 numerators 2^(s sl2 - m) of one row, packed to bf16 pairs (the operand type of the product
 // with V; half a step, 2^-8, of each), their unrounded sum in acc. All on the special-function unit: a
 // polynomial for two pairs in eight, as in the rolling-window kernel, made the kernel 3 % slower (1046 us
-// against 1010 us, 2048 rows of 32 heads on 30720 cached tokens), its own degree 4 instead of 3 (a row sum
+// against 1010 us, 2048 rows of 32 heads, the last of 32768 tokens), its own degree 4 instead of 3 (a row sum
 // has to hold fp32) costing more issue slots than the unit gains.
 __device__ __forceinline__ void numerators(const uint32_t* sh, uint64_t c2, uint64_t nm2, uint32_t* pk,
                                            uint64_t (&acc)[4]) {
