@@ -168,7 +168,7 @@ def test_attention_with_peaked_scores_and_wide_bounds():
     c.check(out, z, True, weight, old)
 
 
-@pytest.mark.parametrize("qs", [[1, 1], [4, 3], [90, 130]])
+@pytest.mark.parametrize("qs", [[1, 1], [4, 3], [13, 9], [27, 32], [90, 130]])
 def test_one_far_larger_score_at_each_place(qs):
     """The running maximum moves by a hundred at one key: at the start, inside and at the end of a
     tile, in the last tile; the others' weights vanish."""
@@ -254,7 +254,10 @@ def test_many_streams():
     ([5000], [130], 2, 2, 128),                  # two units, 40 tiles each, over 80 thread blocks
     ([300] * 20, [32] * 20, 20, 20, 16),         # 32 rows: the last of the single-token form
     ([300] * 20, [33] * 20, 20, 20, 16),         # 33: the first of the chunk form
+    ([3000, 40], [64, 30], 4, 4, 32),            # half a row tile, alone and beside fewer
     ([260, 90, 33, 16, 400], [16, 1, 8, 2, 4], 8, 4, 16),  # 32 rows and fewer in one batch
+    ([900, 64, 2000, 65, 128], [5, 3, 4, 5, 1], 60, 5, 64),  # 12 heads to one: 60 rows and fewer
+    ([300] * 20, [65] * 20, 20, 20, 16),         # just above half a row tile
 ])
 def test_shared_work(kvs, qs, hq, hk, page, causal):
     c = Cache(31, kvs, qs, hq, hk, page)
