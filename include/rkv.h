@@ -351,7 +351,7 @@ int rkv_copy_heads(const rkv_head_copy* runs, int n_runs, int n_heads, void* str
  *
  * What a device array holds is checked on the device: a length outside its bound (0 <=
  * kv_len <= max_kv, 0 <= n_q <= max_q, row ranges inside the tensors) leaves that stream's
- * outputs unwritten, a page id outside [0, n_pages) is never followed (its keys are read from
+ * outputs unwritten (a q_start that decreases somewhere: any stream's), a page id outside [0, n_pages) is never followed (its keys are read from
  * page 0, writes to it are dropped), and both set `status`, read by rkv_paged_poll_status.
  * Slots at and after kv_len may hold anything, NaN included; cached tokens before it have to
  * be finite.
@@ -443,8 +443,8 @@ int rkv_paged_evict(const rkv_page_pool* pool, const rkv_paged_batch* batch, flo
                     long long weight_stride, int keep, int sinks, int recent, int* kept, int* kv_len_out,
                     void* stream);
 
-/* rkv_paged_poll_status - synchronise `stream`, read and clear the device word that
- *  rkv_paged_batch names: RKV_ERR_TIMEOUT (a bounded wait expired), RKV_ERR_PAGE (a length or
+/* rkv_paged_poll_status - synchronise `stream`, read and clear (in its order) the device word
+ *  that rkv_paged_batch names: RKV_ERR_TIMEOUT (a bounded wait expired), RKV_ERR_PAGE (a length or
  *  page id out of bounds) or RKV_OK. Errors: RKV_ERR_ARG, RKV_ERR_CUDA. */
 int rkv_paged_poll_status(unsigned* status, void* stream);
 

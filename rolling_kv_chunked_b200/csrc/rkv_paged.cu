@@ -26,8 +26,9 @@ __global__ void __launch_bounds__(kWriteWarps * 32) paged_write_kernel(const __g
   if (s < 0) return;
   const PagedSeq q = paged_seq(w, s);
   const int lane = threadIdx.x & 31;
-  const int pos = q.kv - q.n_q + (row - q.q0);
-  if (!q.ok || pos < 0) {
+  const int at = row - q.q0;  // the search finds another stream's range where q_start decreases
+  const int pos = q.kv - q.n_q + at;
+  if (!q.ok || at < 0 || at >= q.n_q || pos < 0) {
     if (lane == 0) paged_report(w, kStatusLength);
     return;
   }

@@ -118,11 +118,13 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
   const PagedView& w = p.view;
   const int t = threadIdx.x;
   int blocks = 0;
+  bool falls = false;
   for (int base = 0; base < w.n_seqs; base += kPlanThreads) {
     const int s = base + t;
     int c = 0;
     if (s < w.n_seqs) {
       const PagedSeq q = paged_seq(w, s);
+      falls |= q.n_q < 0;
       if (q.ok)
         c = (q.n_q + p.block_tokens - 1) / p.block_tokens;
       else
@@ -134,7 +136,9 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
     if (base == 0) near_seq[t] = first;
     blocks += total;
   }
-  __syncthreads();
+  // row ranges that overlap (q_start decreases: reported above) may need more blocks than the list holds, or than
+  // 31 bits count: then there is no work
+  if (__syncthreads_or(falls)) blocks = 0;
   // for the weights: the streams with the longest chunks first, so that the last key tiles drawn are short work
   if (p.order != nullptr && t < w.n_seqs) {
     auto length = [&](int s) { return (s + 1 < w.n_seqs ? near_seq[s + 1] : blocks) - near_seq[s]; };
@@ -145,11 +149,6 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
       rank += x > mine || (x == mine && s < t);
     }
     p.order[rank] = t;
-  }
-  // row ranges that overlap (a start below an earlier one) can ask for more than the rows hold
-  if (blocks > p.n_blocks) {
-    if (t == 0) paged_report(w, kStatusLength);
-    blocks = p.n_blocks;
   }
   int tiles = 0, most = 0, least = 1 << 30;
   for (int base = 0; base < blocks; base += kPlanThreads) {
@@ -949,6 +948,7 @@ __global__ void __launch_bounds__(kWThreads, 2)
   int* ticket = reinterpret_cast<int*>(bars + kWbCount + 1);
   ptx::let_next_launch();
   ptx::wait_previous();
+  if (p.work != nullptr && p.work->n_blocks == 0) return;  // the plan found nothing to do
   PagedTiles<kBN> place;
   place.order = p.order;
   place.count(w, false);  // a bad length was reported by the attention

@@ -562,6 +562,81 @@ def test_bad_lengths_and_pages_are_reported_and_not_followed():
             assert c.batch.poll() == rkv.ERR_PAGE
 
 
+@pytest.mark.parametrize("qs", [[2, 1, 2, 1], [40, 9, 130, 3]])
+def test_row_ranges_that_decrease_are_reported(qs):
+    """q_start falls back in the middle: reported by every call, and what lies outside the streams' tokens and the
+    tensors' rows stays as it was."""
+    c = Cache(33, [200, 300, 100, 260], qs, 4, 2, 16, max_q=sum(qs))
+    weight = torch.ones((4, 2, c.max_kv), device="cuda")
+    c.q_start.copy_(torch.tensor([0, c.rows, 1, 3, 3 + qs[3]], dtype=torch.int32))
+    out, z = c.attend(weight=weight)
+    assert c.batch.poll() == rkv.ERR_PAGE
+    assert (out[c.rows:] == 7.0).all() and (z[c.rows:] == 7.0).all()
+    for s, n in enumerate(c.kvs):
+        assert (weight[s, :, n:] == 1).all()
+    k = c.normal(c.rows + c.spare, 2, 128)
+    spare = [p for p in range(c.k.shape[0]) if p not in set(c.table.flatten().tolist())]
+    rkv.paged_write(c.pool, c.batch, k, k)
+    assert c.batch.poll() == rkv.ERR_PAGE
+    assert torch.isnan(c.k[spare]).all()
+    for s, n in enumerate(c.kvs):  # the places behind a stream's last token on its last page
+        if n % 16:
+            assert torch.isnan(c.k[c.table[s, n // 16].long(), :, n % 16:]).all()
+
+
+@pytest.mark.parametrize("qs", [[1, 2, 1], [20, 3, 9], [70, 140, 1]])
+def test_rows_from_the_middle_and_pages_in_two_streams(qs):
+    """The chunk's rows start behind the tensors' first, and two streams hold the same pages at their start; the
+    page lists are columns of a wider tensor."""
+    c = Cache(34, [290, 330, 50], qs, 6, 2, 32)
+    same = 64  # tokens of two pages
+    wide = torch.full((3, c.table.shape[1] + 3), -7, dtype=torch.int32, device="cuda")
+    wide[:, :-3] = c.table
+    wide[1, :2] = wide[0, :2]
+    c.dk[1][:same], c.dv[1][:same] = c.dk[0][:same], c.dv[0][:same]
+    skip = c.spare - 1  # rows before the chunk's; one is left behind it
+    c.q_start += skip
+    q = torch.full_like(c.q, NAN)
+    q[skip:skip + c.rows] = c.q[:c.rows]
+    c.batch = rkv.PagedBatch(wide[:, :-3], c.kv_len, c.q_start, c.max_q, c.max_kv, c.status)
+    old = torch.rand((3, 2, c.max_kv), device="cuda")
+    weight = old.clone()
+    out, z = c.attend(weight=weight, q=q)
+    for t in (out, z):
+        assert (t[:skip] == 7.0).all() and (t[skip + c.rows:] == 7.0).all()
+    c.check(out[skip:], z[skip:], True, weight, old)
+    k, v = c.normal(c.rows + c.spare, 2, 128), c.normal(c.rows + c.spare, 2, 128)
+    rkv.paged_write(c.pool, c.batch, k, v)
+    assert c.batch.poll() == rkv.OK
+    c.table = wide
+    for s, n in enumerate(c.kvs):
+        a, b = c.rows_of(s)
+        assert torch.equal(c.tokens(c.k, s, n)[n - c.qs[s]:], k[skip + a:skip + b])
+        assert torch.equal(c.tokens(c.v, s, n)[n - c.qs[s]:], v[skip + a:skip + b])
+
+
+@pytest.mark.parametrize("qs", [[1, 1, 1], [20, 3, 9], [70, 140, 1]])
+def test_two_graphs_of_one_workspace(qs):
+    """Two captured calls of different pages and rows share a workspace and are replayed in turn."""
+    c = [Cache(35 + i, [500 - 90 * i, 300, 40 + 60 * i], qs, 8, 2, 16) for i in range(2)]
+    size = max(rkv.paged_workspace_bytes(x.pool, x.batch, x.rows + x.spare, 8, True) for x in c)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    weight = [torch.zeros((3, 2, x.max_kv), device="cuda") for x in c]
+    outs = [torch.full_like(x.q, 7.0) for x in c]
+    graphs = []
+    torch.cuda.synchronize()
+    for x, w, o in zip(c, weight, outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            x.attend(lse=False, weight=w, out=o, workspace=ws)
+        graphs.append(g)
+    ws.fill_(255)
+    for i in (0, 1, 1, 0):
+        old = weight[i].clone()
+        graphs[i].replay()
+        c[i].check(outs[i], None, True, weight[i], old)
+
+
 def test_refusals_on_the_device():
     c = Cache(29, [200, 300], [1, 1], 4, 2, 16)
     out = torch.empty_like(c.q)
