@@ -595,10 +595,10 @@ __global__ void __launch_bounds__(kTokenWeightThreads)
   const int sh = blockIdx.x / n_kt;
   const int h = sh % w.kv_heads, s = sh / w.kv_heads;
   const int j0 = (blockIdx.x - sh * n_kt) * kTokenWeightTile + threadIdx.x;
+  ptx::wait_previous();  // before the lengths too: the kernels before this one let it start before they have waited
   const PagedSeq q = paged_seq(w, s);
   float* to = p.weight + (static_cast<long long>(s) * w.kv_heads + h) * p.weight_stride;
   const int fresh = q.kv - q.n_q;  // the chunk's own keys start from zero
-  ptx::wait_previous();
   if (!q.ok || q.n_q == 0 || j0 >= q.kv) return;
   float old[kTokenWeightKeys], sum[kTokenWeightKeys];
 #pragma unroll
