@@ -267,7 +267,7 @@ class PagedBatch:
             if t is not None:
                 _dense(t, i32, shape, dev, where)
         self.page_table, self.kv_len, self.q_start, self.status = page_table, kv_len, q_start, status
-        self.device, self.n_seqs = dev, n
+        self.device, self.n_seqs, self.max_kv = dev, n, max_kv
         self._c = _PagedBatch(_ptr(page_table), _ptr(kv_len), _ptr(q_start), _ptr(status), stride, n, max_q, max_kv)
         self._ref = ctypes.byref(self._c)
 
@@ -316,6 +316,8 @@ def paged_attention(pool: PagePool, batch: PagedBatch, q, out, causal: bool = Tr
     if weight is not None:
         wp = _dense(weight, torch.float32, (batch.n_seqs, pool.kv_heads, None), dev, where)
         width = weight.shape[2]
+        if width < batch.max_kv:
+            _refuse(where)  # here too: a tensor without elements has no address to refuse
     if workspace is None:
         size = paged_workspace_bytes(pool, batch, rows, heads, weight is not None)
         if stream is None:

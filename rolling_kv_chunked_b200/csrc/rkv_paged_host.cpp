@@ -128,7 +128,13 @@ rkv::PagedPlan plan_of(const rkv_page_pool* pool, const rkv_paged_batch* b, int 
   }
   p.score_stride = (b->max_kv + 63LL) / 64 * 64;
   // scores are kept for at most 16 rows: 8 bytes of traffic for each, where reading K again takes 256
-  p.scores = weight && p.slot_rows == 16 ? take(4 * heads * p.score_stride) : -1;
+  p.scores = -1;
+  if (weight && p.slot_rows == 16) {
+    if (p.score_stride > 0 && heads > (1LL << 48) / p.score_stride)
+      p.total = -1;  // no memory holds that, and the sum would pass 64 bits
+    else
+      p.scores = take(4 * heads * p.score_stride);
+  }
   return p;
 }
 
@@ -153,6 +159,7 @@ RKV_API int rkv_paged_write(const rkv_page_pool* pool, const rkv_paged_batch* ba
                             int n_rows, long long k_stride, long long v_stride, void* stream) {
   const int rc = check_batch(pool, batch, n_rows, true);
   if (rc) return rc;
+  if (static_cast<long long>(n_rows) * pool->kv_heads >= (1LL << 31)) return RKV_ERR_UNSUPPORTED;
   if (n_rows == 0 || batch->n_seqs == 0) return RKV_OK;
   if (!aligned16(k) || !aligned16(v) || !row_stride_ok(k_stride, pool->kv_heads) ||
       !row_stride_ok(v_stride, pool->kv_heads))
@@ -259,6 +266,7 @@ RKV_API int rkv_paged_evict(const rkv_page_pool* pool, const rkv_paged_batch* ba
   const int rc = check_batch(pool, batch, 0, false);
   if (rc) return rc;
   if (keep < 1 || sinks < 0 || recent < 0 || static_cast<long long>(sinks) + recent > keep) return RKV_ERR_ARG;
+  if (keep > (1 << 30)) return RKV_ERR_UNSUPPORTED;
   if (batch->n_seqs == 0) return RKV_OK;
   if (!aligned4(weight) || weight_stride < batch->max_kv || !aligned4(kept) || !aligned4(kv_len_out))
     return RKV_ERR_ARG;
@@ -277,10 +285,12 @@ RKV_API int rkv_paged_evict(const rkv_page_pool* pool, const rkv_paged_batch* ba
 
 RKV_API int rkv_paged_poll_status(unsigned* status, void* stream) {
   if (!aligned4(status)) return RKV_ERR_ARG;
-  if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return RKV_ERR_CUDA;
+  // all in the stream's order: a clear on another stream could wipe out what this one's next kernel reports
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
   unsigned word = 0;
-  if (cudaMemcpy(&word, status, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess) return RKV_ERR_CUDA;
-  if (word != 0 && cudaMemset(status, 0, sizeof(word)) != cudaSuccess) return RKV_ERR_CUDA;
+  if (cudaMemcpyAsync(&word, status, sizeof(word), cudaMemcpyDeviceToHost, st) != cudaSuccess) return RKV_ERR_CUDA;
+  if (cudaStreamSynchronize(st) != cudaSuccess) return RKV_ERR_CUDA;
+  if (word != 0 && cudaMemsetAsync(status, 0, sizeof(word), st) != cudaSuccess) return RKV_ERR_CUDA;
   if (word & rkv::kStatusTimeout) return RKV_ERR_TIMEOUT;
   return (word & (rkv::kStatusPage | rkv::kStatusLength)) ? RKV_ERR_PAGE : RKV_OK;
 }

@@ -670,3 +670,22 @@ def test_refusals_on_the_device():
     rkv.paged_attention(c.pool, empty, c.q[:0], out[:0])
     rkv.paged_write(c.pool, empty, c.q[:0, :2], c.q[:0, :2])
     torch.cuda.synchronize()
+
+
+def test_weights_without_columns_are_refused():
+    c = Cache(37, [200, 300], [1, 1], 4, 2, 16)
+    with pytest.raises(rkv.RkvError) as e:
+        c.attend(weight=torch.zeros((2, 2, 0), device="cuda"))
+    assert e.value.code == rkv.ERR_ARG
+
+
+def test_poll_follows_its_stream():
+    """A report that comes after the poll on the same stream is not wiped out by the poll's clear."""
+    c = Cache(38, [200, 300], [1, 1], 4, 2, 16)
+    c.kv_len[1] = 301
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(50):
+            c.attend()
+            assert c.batch.poll() == rkv.ERR_PAGE

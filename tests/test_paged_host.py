@@ -62,6 +62,7 @@ def test_write_refusals():
                dict(vs=-256), dict(vs=260)):
         assert write(**kw) == rkv.ERR_ARG, kw
     assert write(rows=0, k=None, v=None) == rkv.OK
+    assert write(rows=1 << 30) == rkv.ERR_UNSUPPORTED
 
 
 def test_attention_refusals():
@@ -90,6 +91,11 @@ def test_workspace_is_a_host_computation():
     assert size(rows=-1)[0] == rkv.ERR_ARG
     assert size(p=pool(page_tokens=17))[0] == rkv.ERR_UNSUPPORTED
     assert rkv._lib.rkv_paged_workspace(pool(), batch(), 4, 8, 0, None) == rkv.ERR_ARG
+    # scores of 2^28 rows of 4 heads over 2^24 tokens: past any memory, and 64 bits where both grow further
+    far = batch(max_q=1, table_stride=1 << 20, max_kv=1 << 24)
+    assert size(b=far, rows=1 << 28)[0] == rkv.OK
+    assert size(b=far, rows=1 << 28, weight=1)[0] == rkv.ERR_UNSUPPORTED
+    assert size(b=far, rows=2, weight=1)[0] == rkv.OK
 
 
 def test_evict_refusals():
@@ -97,6 +103,8 @@ def test_evict_refusals():
                dict(weight=A + 2), dict(width=63), dict(kept=None), dict(out=None),
                dict(keep=2, sinks=(1 << 31) - 1, recent=(1 << 31) - 1)):
         assert evict(**kw) == rkv.ERR_ARG, kw
+    for keep in ((1 << 30) + 1, (1 << 31) - 1):
+        assert evict(keep=keep) == rkv.ERR_UNSUPPORTED
     assert rkv._lib.rkv_paged_poll_status(None, None) == rkv.ERR_ARG
     assert rkv._lib.rkv_paged_poll_status(A + 2, None) == rkv.ERR_ARG
     assert "page" in rkv.status_string(rkv.ERR_PAGE)
