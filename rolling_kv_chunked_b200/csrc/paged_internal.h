@@ -56,8 +56,8 @@ struct PagedBlock {
   int tiles;      // key tiles, at least 1
   int unused;
 };
-// How the thread blocks share them. In a row: block c of n_ctas walks tiles [c W / n, (c + 1) W / n) of all
-// heads' tiles W. In step (units of nearly one size): every thread block takes `waves` whole units; of the
+// How the thread blocks share them. In a row: block c of n_ctas walks an even share (PagedShares) of
+// all heads' tiles. In step (units of nearly one size): every thread block takes `waves` whole units; of the
 // last n_tail, thread block i < n_tail takes the first `quota` tiles of unit i, and the others share
 // what is left of them, `quota` tiles each, in a row.
 struct PagedShare {  // one thread block's
@@ -67,8 +67,9 @@ struct PagedShare {  // one thread block's
   int unused;
 };
 struct PagedJoin {  // a unit that was shared: parts in slots slot0, slot0 + 1, slot0 + 1 + step, ... (parts 0: none)
-  int b, h, slot0, step, parts;
-  int unused[3];
+  int row0, cnt, h;  // its first row of the chunk tensors, tokens, head
+  int slot0, step, parts;
+  int unused[2];
 };
 struct PagedWork {
   int n_blocks;

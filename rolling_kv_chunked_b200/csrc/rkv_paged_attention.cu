@@ -74,8 +74,6 @@ constexpr uint32_t kIdescPV = ptx::idesc_bf16_f32(kBM, kHeadDim, true);
 
 // ---------------------------------------------------------------- the plan
 constexpr int kPlanThreads = 1024;
-constexpr int kMinTiles = 1;  // key tiles of a thread block's share at least: idle SMs cost more than the merge (6 units of 8 to
-                              // 11 tiles: 25 us with 4, 16 with 1)
 
 // Exclusive sum over the thread block, and its total.
 __device__ __forceinline__ int plan_scan(int x, int* warp_sums, int& total) {
@@ -112,6 +110,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
   __shared__ int sizes[2][32];
   __shared__ int near_seq[kPlanThreads];        // first block of every stream, if there are that few
   __shared__ int near_start[kPlanThreads + 1];  // first tile of every block
+  __shared__ int2 near_rows[kPlanThreads];      // its first row and tokens
   __shared__ int near_rest[kSmCount + 2];
   ptx::let_next_launch();
   ptx::wait_previous();
@@ -172,6 +171,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
     if (b < blocks) p.blocks[b] = k;
     if (base == 0) {
       near_start[t] = k.start;
+      near_rows[t] = make_int2(k.row0, k.cnt);
       if (t == kPlanThreads - 1) near_start[kPlanThreads] = k.start + k.tiles;
     }
     tiles += total;
@@ -197,18 +197,21 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
   const int waves = static_cast<int>(units / kSmCount), n_tail = static_cast<int>(units - static_cast<long long>(waves) * kSmCount);
   const long long first = static_cast<long long>(waves) * kSmCount;  // the first of the last units
   int n = 0;  // thread i < n_tail: tiles of the i-th of them
-  if (t < n_tail) n = tiles_of(static_cast<int>((first + t) % blocks));
+  if (t < n_tail) n = tiles_of(static_cast<int>(first + t - quotient(first + t, blocks) * blocks));
   int tail_tiles;
   plan_scan(n, warp_sums, tail_tiles);
   const int quota = (tail_tiles + kSmCount - 1) / kSmCount;
-  // in step: sizes within an eighth of each other, and shares worth a merge
-  const bool in_step = blocks > 0 && least >= most - most / 8 && (n_tail == 0 || quota >= kMinTiles);
+  // in step: sizes within an eighth of each other
+  const bool in_step = blocks > 0 && least >= most - most / 8;
   int rest_tiles;
   const int rest = plan_scan(max(0, n - quota), warp_sums, rest_tiles);
   if (t <= n_tail) out->rest[t] = near_rest[t] = rest;
   if (t == 0) *p.ticket = 0;
-  const int n_ctas = in_step ? kSmCount
-                             : static_cast<int>(min(static_cast<long long>(kSmCount), max(units, (all + kMinTiles - 1) / kMinTiles)));
+  // in a row: shares down to one tile, since idle SMs cost more than the merge (6 units of 8 to 11 tiles: 16 us; 25
+  // with four tiles at least)
+  PagedShares row;
+  row.split(all, kSmCount);
+  const int n_ctas = in_step ? kSmCount : row.n;
   if (t == 0) {
     out->n_blocks = blocks;
     out->n_ctas = n_ctas;
@@ -221,6 +224,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
   if (t >= kSmCount) return;
   PagedShare mine = {};
   PagedJoin join = {};
+  int joined = 0;  // its block
   if (in_step) {
     const int helpers = kSmCount - n_tail;
     if (t < n_tail) {
@@ -228,8 +232,8 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
       const int r0 = near_rest[t], r1 = near_rest[t + 1];
       if (r1 > r0) {
         const int j0 = min(helpers - 1, r0 / quota), j1 = min(helpers - 1, (r1 - 1) / quota);
-        join.h = static_cast<int>((first + t) / blocks);
-        join.b = static_cast<int>(first + t - static_cast<long long>(join.h) * blocks);
+        join.h = static_cast<int>(quotient(first + t, blocks));
+        joined = static_cast<int>(first + t - static_cast<long long>(join.h) * blocks);
         join.slot0 = 2 * t + j0;
         join.step = 1;
         join.parts = j1 - j0 + 2;
@@ -244,23 +248,25 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
       }
     }
   } else if (t < n_ctas) {
-    auto border = [&](int c) { return all * c / n_ctas; };
-    const long long x = border(t);
-    mine.left = border(t + 1) - x;
-    mine.h = static_cast<int>(x / tiles);
+    const long long x = row.start(t);
+    mine.left = row.start(t + 1) - x;
+    mine.h = static_cast<int>(quotient(x, tiles));
     const int y = static_cast<int>(x - static_cast<long long>(mine.h) * tiles);
     mine.b = last_at_most(near_start, &p.blocks[0].start, sizeof(PagedBlock) / 4, blocks, y);
     mine.t = y - start_of(mine.b);
     // the unit that this share's start cuts, if it is the first border inside it
-    const long long begin = x - mine.t, end = begin + tiles_of(mine.b);
-    if (mine.t > 0 && border(t - 1) <= begin) {
-      join.b = mine.b;
+    const long long begin = x - mine.t;
+    if (mine.t > 0 && row.start(t - 1) <= begin) {
+      joined = mine.b;
       join.h = mine.h;
       join.slot0 = 2 * t - 1;
       join.step = 2;
-      join.parts = 2;
-      while (t + join.parts - 1 < n_ctas && border(t + join.parts - 1) < end) ++join.parts;
+      join.parts = row.owner(begin + tiles_of(mine.b) - 1) - t + 2;
     }
+  }
+  if (join.parts > 0) {
+    join.row0 = blocks <= kPlanThreads ? near_rows[joined].x : p.blocks[joined].row0;
+    join.cnt = blocks <= kPlanThreads ? near_rows[joined].y : p.blocks[joined].cnt;
   }
   out->share[t] = mine;
   out->join[t] = join;
@@ -311,7 +317,7 @@ struct PagedWalk {
     u.last_valid = min(kBN, u.k.keys - (u.t1 - 1) * kBN);
   }
   __device__ __forceinline__ void at_unit(long long n) {
-    h = static_cast<int>(n / n_blocks);
+    h = static_cast<int>(quotient(n, n_blocks));
     b = static_cast<int>(n - static_cast<long long>(h) * n_blocks);
   }
   __device__ __forceinline__ bool next(PagedUnit& u) {
@@ -821,48 +827,70 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------- units that were shared
-// Their parts are added up in order, one warp per row. (Shared in a row: the second slot of the thread block that
-// began the unit, then the first slots of those after it; in step: the first part's, then the helpers'.)
+// Their parts are added up in order, one warp per row, two rows at a time. (Shared in a row: the second slot of the
+// thread block that began the unit, then the first slots of those after it; in step: the first part's, then the
+// helpers'.) Eight thread blocks per unit take every eighth run of eight rows; three loads in a row bound it, so all
+// parts' loads of a step leave together (within 1 us of four or sixteen blocks per unit at every size).
 constexpr int kJoinThreads = 256;
-constexpr int kJoinSlices = kPagedPartRows / (kJoinThreads / 32);  // a row per warp
+constexpr int kJoinSlices = 8;
+constexpr int kJoinStep = kJoinSlices * (kJoinThreads / 32);  // rows from one of a warp's to its next
 
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ PagedAttnParams p) {
   ptx::let_next_launch();
   ptx::wait_previous();
   const PagedJoin join = p.work->join[blockIdx.x / kJoinSlices];
   if (join.parts == 0) return;
-  const PagedBlock k = p.blocks[join.b];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tpt = kBM / p.group;
-  const int rr = blockIdx.x % kJoinSlices * (kJoinThreads / 32) + warp;  // row of the unit
-  const int tile = rr / kBM, r = rr % kBM, tok = r / p.group;
-  if (r >= tpt * p.group || tile * tpt + tok >= k.cnt) return;
-  float m = kNoKey, l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int row0 = blockIdx.x % kJoinSlices * (kJoinThreads / 32) + warp;  // first row of the unit
+#pragma unroll 1
+  for (int k = row0; k < kPagedPartRows; k += 2 * kJoinStep) {
+    int tok[2], head[2];
+    bool live[2];
+    float m[2], l[2];
+    float4 o[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int rr = k + e * kJoinStep, r = rr % kBM, t = r / p.group;
+      tok[e] = rr / kBM * tpt + t;
+      head[e] = join.h * p.group + r - t * p.group;
+      live[e] = t < tpt && tok[e] < join.cnt;
+      m[e] = kNoKey;
+      l[e] = 0.f;
+      o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    if (!live[0] && !live[1]) continue;
 #pragma unroll 4
-  for (int i = 0; i < join.parts; ++i) {
-    const long long at = static_cast<long long>(i == 0 ? join.slot0 : join.slot0 + 1 + (i - 1) * join.step) * kPagedPartRows + rr;
-    const float2 e = p.part_ml[at];
-    const float4 y = *reinterpret_cast<const float4*>(p.part + at * kHeadDim + lane * 4);
-    const float mn = fmaxf(m, e.x);
-    const float f = ptx::ex2(m - mn), f2 = ptx::ex2(e.x - mn);
-    m = mn;
-    l = l * f + e.y * f2;
-    o.x = o.x * f + y.x * f2;
-    o.y = o.y * f + y.y * f2;
-    o.z = o.z * f + y.z * f2;
-    o.w = o.w * f + y.w * f2;
-  }
-  const long long row = k.row0 + tile * tpt + tok;
-  const int head = join.h * p.group + r - tok * p.group;
-  const float inv = l == 0.f ? 0.f : 1.0f / l;
-  *reinterpret_cast<uint2*>(p.out + row * p.out_stride + head * kHeadDim + lane * 4) =
-      make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-  if (lane == 0) {
-    const float z = l > 0.f ? m + log2f(l) : l == 0.f ? -INFINITY : l;
-    const long long rh = row * p.q_heads + head;
-    if (p.lse != nullptr) p.lse[rh] = z * kLn2;
-    if (p.lse2 != nullptr) p.lse2[rh] = z;
+    for (int i = 0; i < join.parts; ++i) {
+      const long long at = static_cast<long long>(i == 0 ? join.slot0 : join.slot0 + 1 + (i - 1) * join.step) * kPagedPartRows + k;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {  // a row that is not live reads what its place holds, and writes nothing
+        const float2 x = p.part_ml[at + e * kJoinStep];
+        const float4 y = *reinterpret_cast<const float4*>(p.part + (at + e * kJoinStep) * kHeadDim + lane * 4);
+        const float mn = fmaxf(m[e], x.x);
+        const float f = ptx::ex2(m[e] - mn), f2 = ptx::ex2(x.x - mn);
+        m[e] = mn;
+        l[e] = l[e] * f + x.y * f2;
+        o[e].x = o[e].x * f + y.x * f2;
+        o[e].y = o[e].y * f + y.y * f2;
+        o[e].z = o[e].z * f + y.z * f2;
+        o[e].w = o[e].w * f + y.w * f2;
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      if (!live[e]) continue;
+      const long long row = join.row0 + tok[e];
+      const float inv = l[e] == 0.f ? 0.f : 1.0f / l[e];
+      *reinterpret_cast<uint2*>(p.out + row * p.out_stride + head[e] * kHeadDim + lane * 4) =
+          make_uint2(pack_bf16x2(o[e].x * inv, o[e].y * inv), pack_bf16x2(o[e].z * inv, o[e].w * inv));
+      if (lane == 0) {
+        const float z = l[e] > 0.f ? m[e] + log2f(l[e]) : l[e] == 0.f ? -INFINITY : l[e];
+        const long long rh = row * p.q_heads + head[e];
+        if (p.lse != nullptr) p.lse[rh] = z * kLn2;
+        if (p.lse2 != nullptr) p.lse2[rh] = z;
+      }
+    }
   }
 }
 

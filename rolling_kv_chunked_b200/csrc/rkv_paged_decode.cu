@@ -16,7 +16,7 @@
 // without a pause at unit borders; units that a border cuts are left as partial rows for
 // paged_token_join_kernel. (Parts of a fixed length, a thread block each: 238 us for 48 streams of 49 to
 // 16384 tokens and 101 us for one of 131071 at the length that suits both, 221 and 91 us at the one that
-// suits each.) Every thread block counts the tiles for itself: one probe of 32 lengths per warp step.
+// suits each; shares of four tiles at least: 11 us for 1590 tokens where single tiles take 8.) Every thread block counts the tiles for itself: one probe of 32 lengths per warp step.
 #include <mutex>
 
 #include "numeric.cuh"
@@ -37,7 +37,6 @@ constexpr int kSmemMerge = kStages * kStageBytes;                              /
 constexpr int kSmemMl = kSmemMerge + kWarps * kMergeRows * kHeadDim * 4;       // [warp][row]: reference, sum
 constexpr int kSmemDecodeBar = kSmemMl + 128 * 8;
 constexpr int kDecodeSmem = kSmemDecodeBar + 128 + 1024;
-constexpr int kMinTiles = 1;  // tiles of a share at least (one stream of 1590 tokens: 11 us with 4, 8 with 1)
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 8.0f;  // log2: the running reference follows a maximum only past this
 constexpr float kNoKey = -1e30f;  // reference (log2) of a row that has seen no key
@@ -57,27 +56,22 @@ struct TokenUnit {
 
 // The shares of all units' tiles, and one thread block's way through its own. Whole warps call these.
 struct TokenWalk : PagedTiles<kTileKeys> {
-  long long left;        // tiles still to walk
-  long long each;        // tiles of a share; the first `more` shares have one more
-  int n, more;           // shares
+  long long left;  // tiles still to walk
+  PagedShares of;
 
   __device__ __forceinline__ void share(const PagedView& w) {
     count(w, blockIdx.x == 0);
-    n = static_cast<int>(min(static_cast<long long>(2 * kSmCount), (all + kMinTiles - 1) / kMinTiles));
-    each = n > 0 ? quotient(all, n) : 0;
-    more = static_cast<int>(all - each * n);
+    of.split(all, 2 * kSmCount);
   }
-  __device__ __forceinline__ long long start(int c) const { return each * c + min(c, more); }
   // What the join has to do where share c starts: nothing unless this is the first border inside a unit.
   __device__ __forceinline__ PagedCut cut(int c) const {
     PagedCut r = {};
-    const long long x = start(c), first = x - t, end = first + tiles;
-    if (t == 0 || start(c - 1) > first) return r;
+    const long long first = of.start(c) - t;
+    if (t == 0 || of.start(c - 1) > first) return r;
     r.row0 = q.q0;
     r.n_q = q.n_q;
     r.h = h;
-    r.parts = 2;
-    while (c + r.parts - 1 < n && start(c + r.parts - 1) < end) ++r.parts;
+    r.parts = of.owner(first + tiles - 1) - c + 2;
     return r;
   }
   __device__ __forceinline__ bool next(const PagedView& w, TokenUnit& u) {
@@ -441,12 +435,12 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
   if (cta == 0 && threadIdx.x == 0) *p.ticket = 0;
   TokenWalk walk;
   walk.share(w);
-  if (cta >= walk.n) {
+  if (cta >= walk.of.n) {
     if (threadIdx.x == 0) p.cuts[cta] = PagedCut{};
     return;
   }
-  walk.left = walk.start(cta + 1) - walk.start(cta);
-  walk.go_to(w, walk.start(cta));
+  walk.left = walk.of.start(cta + 1) - walk.of.start(cta);
+  walk.go_to(w, walk.of.start(cta));
   if (threadIdx.x == 0) p.cuts[cta] = walk.cut(cta);
   __syncthreads();
   TokenUnit u;
@@ -546,7 +540,7 @@ __global__ void __launch_bounds__(kTokenJoinWarps * 32)
     o.w = o.w * f + y.w * f2;
   };
   if (team < teams) {
-#pragma unroll 4
+#pragma unroll 8
     for (int i = team * 2 + (lane >> 4); i < cut.parts; i += teams * 2) {
       const long long at = (i == 0 ? 2LL * c - 1 : 2LL * (c - 1 + i)) * p.slot_rows + row0 + r;
       add(p.part_ml[at], *reinterpret_cast<const float4*>(p.part + at * kHeadDim + col));
