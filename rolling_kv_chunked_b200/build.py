@@ -26,7 +26,7 @@ LIB = os.path.join(HERE, "librkv.so")
 SYNTH_LIB = os.path.join(ROOT, "synth", "libsynth.so")
 
 CU_SOURCES = ["rkv_kernels.cu", "rkv_attention.cu", "rkv_noalloc.cu", "rkv_paged.cu",
-              "rkv_paged_decode.cu", "rkv_paged_attention.cu"]
+              "rkv_paged_decode.cu", "rkv_paged_attention.cu", "rkv_paged_join.cu"]
 CPP_SOURCES = ["rkv_host.cpp", "rkv_paged_host.cpp"]
 HEADERS = ["ptx_sm100.cuh", "ptx_warp.cuh", "numeric.cuh", "attention_tile.cuh", "paged.cuh", "rkv_internal.h",
            "paged_internal.h", "tensor_map.h"]

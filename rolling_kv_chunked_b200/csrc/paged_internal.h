@@ -39,8 +39,10 @@ struct PagedPlan {
   int slot_rows;     // single-token form: rows of a stream and KV head, rounded up to 16 or 32; 0: chunk form
   int block_tokens;  // chunk form: tokens of one unit of rows
   int n_blocks;      // and such units of one KV head in the batch at most
-  long long lse, part, part_ml, scores, cuts, blocks, work, seq_first, order, ticket, total;  // -1: not used
+  long long lse, part, part_ml, scores, joins, blocks, work, seq_first, order, ticket, total;  // -1: not used
   long long score_stride;
+  int n_joins, part_rows, join_rows;
+  long long max_units;  // units of work at most
 };
 
 constexpr int kPagedRows = 32;  // rows of the single-token form at most
@@ -66,7 +68,8 @@ struct PagedShare {  // one thread block's
   int i, pos;      // in step, sharing leftovers: the last unit it begins in, and its first leftover tile
   int unused;
 };
-struct PagedJoin {  // a unit that was shared: parts in slots slot0, slot0 + 1, slot0 + 1 + step, ... (parts 0: none)
+// A unit that thread blocks shared: parts in slots slot0, slot0 + 1, slot0 + 1 + step, ... (parts 0: none)
+struct __align__(16) PagedJoin {
   int row0, cnt, h;  // its first row of the chunk tensors, tokens, head
   int slot0, step, parts;
   int unused[2];
@@ -78,11 +81,6 @@ struct PagedWork {
   int waves, n_tail, quota;
   int rest[kSmCount + 2];  // in step: tiles left of the last units before unit i
   PagedShare share[kSmCount];
-  PagedJoin join[kSmCount];
-};
-// Single-token form: the unit that the start of a share cuts (n_q 0: none, or an earlier border cuts it).
-struct PagedCut {
-  int row0, n_q, h, parts;
 };
 constexpr int kPagedMaxOrder = 1024;  // streams that the plan puts in order at most
 constexpr int kPagedPartRows = 256;  // rows of a partial result of the chunk form
@@ -101,7 +99,7 @@ struct PagedAttnParams {
   float* part;      // unnormalised sums of p v of cut units: [4 * kSmCount][slot_rows][128] (single-token
                     // form) or [2 * kSmCount][kPagedPartRows][128]
   float2* part_ml;  // the same rows: reference (log2) and sum of p
-  PagedCut* cuts;      // single-token form: [2 * kSmCount]
+  PagedJoin* joins;    // [n_joins], an entry per thread block of the attention
   PagedBlock* blocks;  // chunk form: [n_blocks]
   PagedWork* work;
   unsigned* ticket;    // units that the chunks' weight kernel has drawn
@@ -109,6 +107,8 @@ struct PagedAttnParams {
   int* order;          // chunk form: [n_seqs], the streams by falling chunk length; null: as they come
   float* scores;    // [n_rows][q_heads][score_stride]: log2 scores of the single-token form; null: not kept
   long long score_stride;
+  int n_joins, part_rows, join_rows;  // join_rows: rows of a part that are used at most
+  long long max_units;
   int slot_rows;                // single-token form
   int block_tokens, n_blocks;  // chunk form
   unsigned long long wait_limit_ns;
@@ -132,6 +132,8 @@ cudaError_t launch_paged_decode(const CUtensorMap& tm_k, const CUtensorMap& tm_v
 // min(page_tokens, kKeyBox) tokens.
 cudaError_t launch_paged_chunk(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                                const PagedAttnParams& p, cudaStream_t stream);
+// adds up what the thread blocks of either left in parts
+cudaError_t launch_paged_join(const PagedAttnParams& p, cudaStream_t stream);
 cudaError_t launch_paged_weight(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const PagedAttnParams& p,
                                 cudaStream_t stream);
 cudaError_t launch_paged_token_weight(const PagedAttnParams& p, cudaStream_t stream);

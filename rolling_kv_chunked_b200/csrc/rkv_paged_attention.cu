@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
     join.cnt = blocks <= kPlanThreads ? near_rows[joined].y : p.blocks[joined].cnt;
   }
   out->share[t] = mine;
-  out->join[t] = join;
+  p.joins[t] = join;
 }
 
 // In step: the thread block (of those past n_tail, counted from 0) that takes leftover tile y.
@@ -826,74 +826,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 9) ptx::tmem_dealloc(tmem, 512);
 }
 
-// ---------------------------------------------------------------- units that were shared
-// Their parts are added up in order, one warp per row, two rows at a time. (Shared in a row: the second slot of the
-// thread block that began the unit, then the first slots of those after it; in step: the first part's, then the
-// helpers'.) Eight thread blocks per unit take every eighth run of eight rows; three loads in a row bound it, so all
-// parts' loads of a step leave together (within 1 us of four or sixteen blocks per unit at every size).
-constexpr int kJoinThreads = 256;
-constexpr int kJoinSlices = 8;
-constexpr int kJoinStep = kJoinSlices * (kJoinThreads / 32);  // rows from one of a warp's to its next
-
-__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ PagedAttnParams p) {
-  ptx::let_next_launch();
-  ptx::wait_previous();
-  const PagedJoin join = p.work->join[blockIdx.x / kJoinSlices];
-  if (join.parts == 0) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int tpt = kBM / p.group;
-  const int row0 = blockIdx.x % kJoinSlices * (kJoinThreads / 32) + warp;  // first row of the unit
-#pragma unroll 1
-  for (int k = row0; k < kPagedPartRows; k += 2 * kJoinStep) {
-    int tok[2], head[2];
-    bool live[2];
-    float m[2], l[2];
-    float4 o[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int rr = k + e * kJoinStep, r = rr % kBM, t = r / p.group;
-      tok[e] = rr / kBM * tpt + t;
-      head[e] = join.h * p.group + r - t * p.group;
-      live[e] = t < tpt && tok[e] < join.cnt;
-      m[e] = kNoKey;
-      l[e] = 0.f;
-      o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-    if (!live[0] && !live[1]) continue;
-#pragma unroll 4
-    for (int i = 0; i < join.parts; ++i) {
-      const long long at = static_cast<long long>(i == 0 ? join.slot0 : join.slot0 + 1 + (i - 1) * join.step) * kPagedPartRows + k;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {  // a row that is not live reads what its place holds, and writes nothing
-        const float2 x = p.part_ml[at + e * kJoinStep];
-        const float4 y = *reinterpret_cast<const float4*>(p.part + (at + e * kJoinStep) * kHeadDim + lane * 4);
-        const float mn = fmaxf(m[e], x.x);
-        const float f = ptx::ex2(m[e] - mn), f2 = ptx::ex2(x.x - mn);
-        m[e] = mn;
-        l[e] = l[e] * f + x.y * f2;
-        o[e].x = o[e].x * f + y.x * f2;
-        o[e].y = o[e].y * f + y.y * f2;
-        o[e].z = o[e].z * f + y.z * f2;
-        o[e].w = o[e].w * f + y.w * f2;
-      }
-    }
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      if (!live[e]) continue;
-      const long long row = join.row0 + tok[e];
-      const float inv = l[e] == 0.f ? 0.f : 1.0f / l[e];
-      *reinterpret_cast<uint2*>(p.out + row * p.out_stride + head[e] * kHeadDim + lane * 4) =
-          make_uint2(pack_bf16x2(o[e].x * inv, o[e].y * inv), pack_bf16x2(o[e].z * inv, o[e].w * inv));
-      if (lane == 0) {
-        const float z = l[e] > 0.f ? m[e] + log2f(l[e]) : l[e] == 0.f ? -INFINITY : l[e];
-        const long long rh = row * p.q_heads + head[e];
-        if (p.lse != nullptr) p.lse[rh] = z * kLn2;
-        if (p.lse2 != nullptr) p.lse2[rh] = z;
-      }
-    }
-  }
-}
-
 // ---------------------------------------------------------------------------------------------
 // Attention weight of chunks. With z the rows' log-sum-exp from the attention before, key j of KV
 // head h gathers sum over the group's rows i that see it of 2^(s_ij - z_i). The product is
@@ -1163,7 +1095,6 @@ cudaError_t launch_paged_chunk(const CUtensorMap& tm_q, const CUtensorMap& tm_k,
   err = launch_after(paged_plan_kernel, 1, kPlanThreads, 0, stream, p);
   if (err == cudaSuccess)
     err = launch_after(paged_chunk_kernel, kSmCount, kThreads, kSmemBytes, stream, tm_q, tm_k, tm_v, p);
-  if (err == cudaSuccess) err = launch_after(paged_join_kernel, kSmCount * kJoinSlices, kJoinThreads, 0, stream, p);
   return err;
 }
 

@@ -14,7 +14,7 @@
 // A unit of work is one stream and KV head. Lengths differ, so all units' tiles, stream after stream and head
 // after head, are shared evenly by the 296 thread blocks that fit the card at once, each walking its share
 // without a pause at unit borders; units that a border cuts are left as partial rows for
-// paged_token_join_kernel. (Parts of a fixed length, a thread block each: 238 us for 48 streams of 49 to
+// paged_join_kernel. (Parts of a fixed length, a thread block each: 238 us for 48 streams of 49 to
 // 16384 tokens and 101 us for one of 131071 at the length that suits both, 221 and 91 us at the one that
 // suits each; shares of four tiles at least: 11 us for 1590 tokens where single tiles take 8.) Every thread block counts the tiles for itself: one probe of 32 lengths per warp step.
 #include <mutex>
@@ -64,13 +64,16 @@ struct TokenWalk : PagedTiles<kTileKeys> {
     of.split(all, 2 * kSmCount);
   }
   // What the join has to do where share c starts: nothing unless this is the first border inside a unit.
-  __device__ __forceinline__ PagedCut cut(int c) const {
-    PagedCut r = {};
+  __device__ __forceinline__ PagedJoin join(int c) const {
+    PagedJoin r = {};
     const long long first = of.start(c) - t;
     if (t == 0 || of.start(c - 1) > first) return r;
     r.row0 = q.q0;
-    r.n_q = q.n_q;
+    r.cnt = q.n_q;
     r.h = h;
+    // the second slot of thread block c - 1, then the first slots of c, c + 1, ... as far as the unit goes
+    r.slot0 = 2 * c - 1;
+    r.step = 2;
     r.parts = of.owner(first + tiles - 1) - c + 2;
     return r;
   }
@@ -431,18 +434,17 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
     }
     ptx::fence_mbar_init();
   }
+  __syncthreads();  // the last one: from here on every warp finds its way by itself
   ptx::wait_previous();
   if (cta == 0 && threadIdx.x == 0) *p.ticket = 0;
   TokenWalk walk;
   walk.share(w);
   if (cta >= walk.of.n) {
-    if (threadIdx.x == 0) p.cuts[cta] = PagedCut{};
+    if (threadIdx.x == 0) p.joins[cta] = PagedJoin{};
     return;
   }
   walk.left = walk.of.start(cta + 1) - walk.of.start(cta);
   walk.go_to(w, walk.of.start(cta));
-  if (threadIdx.x == 0) p.cuts[cta] = walk.cut(cta);
-  __syncthreads();
   TokenUnit u;
 
   if (warp == kWarps) {
@@ -491,6 +493,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
 
   // -------------------------------------------------------------- consumers
   // a unit takes the fewest row tiles that hold its rows: with few rows all four warps share the tokens
+  if (threadIdx.x == 0) p.joins[cta] = walk.join(cta);
   bool ok = true;
   int g = 0;
   while (walk.next(w, u)) {
@@ -501,77 +504,6 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
       token_unit<2>(p, u, smem, full, empty, g, ok);
   }
   if (!ok && lane == 0) paged_report(w, kStatusTimeout);
-}
-
-// ---------------------------------------------------------------- units that were cut
-// The unit that the start of share c cuts, if it is the first border inside that unit; its parts are the
-// second slot of thread block c - 1, then the first slots of c, c + 1, ... as far as the unit goes. With
-// references m_i, sums l_i and unnormalised outputs o_i of the parts:
-//   m = max m_i, out = sum_i o_i 2^(m_i - m) / sum_i l_i 2^(m_i - m), in the order of the parts.
-// A block takes 64 columns; sixteen lanes hold a row's, so a warp reads two parts at once, and the warps that
-// the unit's rows leave over (two per row for 8 rows, four for 4) take their share of the parts: all loads
-// leave together. (A warp per row, part after part: 13 us of 96 for 8 rows in 37 parts.)
-constexpr int kTokenJoinWarps = 16;  // of 16 rows a block; more rows take more blocks
-
-__global__ void __launch_bounds__(kTokenJoinWarps * 32)
-    paged_token_join_kernel(const __grid_constant__ PagedAttnParams p) {
-  __shared__ float4 sum[kTokenJoinWarps][16];
-  __shared__ float2 sum_ml[kTokenJoinWarps];
-  ptx::let_next_launch();
-  const int c = blockIdx.x / 2 + 1, col = (blockIdx.x & 1) * 64 + (threadIdx.x & 15) * 4;
-  const int row0 = blockIdx.y * 16;
-  ptx::wait_previous();  // in every thread block, so that the kernel after this one may rely on it
-  const PagedCut cut = p.cuts[c];
-  const int rows = min(16, cut.n_q * p.group - row0);  // of this block
-  if (rows <= 0) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int teams = kTokenJoinWarps / rows;
-  const int r = warp % rows, team = warp / rows;
-  float m = kNoKey, l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto add = [&](float2 e, float4 y) {
-    const float mn = fmaxf(m, e.x);
-    const float f = ptx::ex2(m - mn), f2 = ptx::ex2(e.x - mn);
-    m = mn;
-    l = l * f + e.y * f2;
-    o.x = o.x * f + y.x * f2;
-    o.y = o.y * f + y.y * f2;
-    o.z = o.z * f + y.z * f2;
-    o.w = o.w * f + y.w * f2;
-  };
-  if (team < teams) {
-#pragma unroll 8
-    for (int i = team * 2 + (lane >> 4); i < cut.parts; i += teams * 2) {
-      const long long at = (i == 0 ? 2LL * c - 1 : 2LL * (c - 1 + i)) * p.slot_rows + row0 + r;
-      add(p.part_ml[at], *reinterpret_cast<const float4*>(p.part + at * kHeadDim + col));
-    }
-  }
-  float2 e;
-  float4 y;
-  e.x = __shfl_down_sync(0xffffffffu, m, 16);
-  e.y = __shfl_down_sync(0xffffffffu, l, 16);
-  y.x = __shfl_down_sync(0xffffffffu, o.x, 16);
-  y.y = __shfl_down_sync(0xffffffffu, o.y, 16);
-  y.z = __shfl_down_sync(0xffffffffu, o.z, 16);
-  y.w = __shfl_down_sync(0xffffffffu, o.w, 16);
-  add(e, y);
-  if (lane < 16) sum[warp][lane] = o;
-  if (lane == 0) sum_ml[warp] = make_float2(m, l);
-  __syncthreads();
-  if (team != 0 || lane >= 16) return;
-  for (int i = 1; i < teams; ++i) add(sum_ml[i * rows + r], sum[i * rows + r][lane]);
-  const int tok = (row0 + r) / p.group;
-  const long long row = cut.row0 + tok;
-  const int head = cut.h * p.group + row0 + r - tok * p.group;
-  const float inv = l == 0.f ? 0.f : 1.0f / l;
-  *reinterpret_cast<uint2*>(p.out + row * p.out_stride + head * kHeadDim + col) =
-      make_uint2(pack2(o.x * inv, o.y * inv), pack2(o.z * inv, o.w * inv));
-  if (col == 0) {
-    const float z = l > 0.f ? m + log2f(l) : l == 0.f ? -INFINITY : l;
-    const long long rh = row * p.q_heads + head;
-    if (p.lse != nullptr) p.lse[rh] = z * kLn2;
-    if (p.lse2 != nullptr) p.lse2[rh] = z;
-  }
 }
 
 // ---------------------------------------------------------------- attention weight of single tokens
@@ -649,10 +581,7 @@ cudaError_t launch_paged_decode(const CUtensorMap& tm_k, const CUtensorMap& tm_v
     }
   }
   const auto kernel = p.slot_rows == 16 ? paged_decode_kernel<1> : paged_decode_kernel<2>;
-  err = launch_after(kernel, 2 * kSmCount, kDecodeThreads, kDecodeSmem, stream, tm_k, tm_v, p);
-  if (err != cudaSuccess) return err;
-  const dim3 joins(2 * (2 * kSmCount - 1), static_cast<unsigned>(p.slot_rows / 16));
-  return launch_after(paged_token_join_kernel, joins, kTokenJoinWarps * 32, 0, stream, p);
+  return launch_after(kernel, 2 * kSmCount, kDecodeThreads, kDecodeSmem, stream, tm_k, tm_v, p);
 }
 
 }  // namespace rkv

@@ -113,14 +113,18 @@ rkv::PagedPlan plan_of(const rkv_page_pool* pool, const rkv_paged_batch* b, int 
     return at;
   };
   p.lse = weight ? take(4 * heads) : -1;
-  p.cuts = p.blocks = p.work = p.seq_first = p.order = -1;
-  const long long rows = p.slot_rows ? 4LL * rkv::kSmCount * p.slot_rows : 2LL * rkv::kSmCount * rkv::kPagedPartRows;
+  p.blocks = p.work = p.seq_first = p.order = -1;
+  p.n_joins = p.slot_rows ? 2 * rkv::kSmCount : rkv::kSmCount;  // thread blocks of the attention
+  p.part_rows = p.slot_rows ? p.slot_rows : rkv::kPagedPartRows;
+  // the rows of one tile, or two
+  p.join_rows = b->max_q <= rkv::kQueryBox / group ? static_cast<int>(most) : rkv::kPagedPartRows;
+  p.max_units = static_cast<long long>(p.slot_rows ? b->n_seqs : p.n_blocks) * pool->kv_heads;
+  const long long rows = 2LL * p.n_joins * p.part_rows;
   p.part = take(4 * rows * kHeadDim);
   p.part_ml = take(8 * rows);
   p.ticket = take(4);
-  if (p.slot_rows) {
-    p.cuts = take(2LL * rkv::kSmCount * sizeof(rkv::PagedCut));
-  } else {
+  p.joins = take(static_cast<long long>(sizeof(rkv::PagedJoin)) * p.n_joins);
+  if (!p.slot_rows) {
     p.blocks = take(static_cast<long long>(sizeof(rkv::PagedBlock)) * p.n_blocks);
     p.work = take(sizeof(rkv::PagedWork));
     p.seq_first = take(4LL * b->n_seqs);
@@ -224,7 +228,11 @@ RKV_API int rkv_paged_attention(const rkv_page_pool* pool, const rkv_paged_batch
   p.part = reinterpret_cast<float*>(ws + plan.part);
   p.part_ml = reinterpret_cast<float2*>(ws + plan.part_ml);
   p.ticket = reinterpret_cast<unsigned*>(ws + plan.ticket);
-  if (plan.cuts >= 0) p.cuts = reinterpret_cast<rkv::PagedCut*>(ws + plan.cuts);
+  p.joins = reinterpret_cast<rkv::PagedJoin*>(ws + plan.joins);
+  p.n_joins = plan.n_joins;
+  p.part_rows = plan.part_rows;
+  p.join_rows = plan.join_rows;
+  p.max_units = plan.max_units;
   if (plan.blocks >= 0) {
     p.blocks = reinterpret_cast<rkv::PagedBlock*>(ws + plan.blocks);
     p.work = reinterpret_cast<rkv::PagedWork*>(ws + plan.work);
@@ -249,6 +257,7 @@ RKV_API int rkv_paged_attention(const rkv_page_pool* pool, const rkv_paged_batch
       return RKV_ERR_CUDA;
   }
   err = plan.slot_rows ? rkv::launch_paged_decode(tm_k, tm_v, p, st) : rkv::launch_paged_chunk(tm_q, tm_k, tm_v, p, st);
+  if (err == cudaSuccess) err = rkv::launch_paged_join(p, st);
   if (err == cudaSuccess && weigh) {
     if (from_scores) {
       err = rkv::launch_paged_token_weight(p, st);

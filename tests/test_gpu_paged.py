@@ -267,6 +267,22 @@ def test_shared_work(kvs, qs, hq, hk, page, causal):
     c.check(out, z, causal, weight, old)
 
 
+@pytest.mark.parametrize("kvs,qs,hq,hk", [
+    ([20000], [1], 1, 1),                    # one row in 296 parts
+    ([20000], [1], 16, 1),
+    ([19000, 37], [5, 1], 6, 1),             # 30 rows, and 6 in one part
+    ([9000, 9000, 300], [1, 2, 1], 14, 2),   # six units: 7 and 14 rows
+    ([15000], [1], 128, 1),                  # 128 rows in 118 parts
+    ([9001, 700], [50, 40], 10, 2),          # two tiles of rows, 125 of 128 used, and a part of them
+    ([5000] * 9, [60] * 9, 4, 2),            # 18 units: the last that are gathered
+    ([5000] * 19, [60] * 19, 2, 1),          # 19: the first the usual way
+])
+def test_few_units_in_many_parts(kvs, qs, hq, hk):
+    c = Cache(39, kvs, qs, hq, hk, 32)
+    out, z = c.attend()
+    c.check(out, z, True)
+
+
 def test_many_streams_with_chunks():
     """More streams, and more blocks of rows, than the plan holds in shared memory."""
     n = 1100
