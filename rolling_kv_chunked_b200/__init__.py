@@ -186,20 +186,19 @@ def _refuse(where: str):
     raise RkvError(ERR_ARG, where)
 
 
-def _dense(t, dtype, shape, device, where: str):
-    """Pointer of a contiguous GPU tensor of this type and shape (None: any extent); refused otherwise."""
-    if (t.dtype is not dtype or not t.is_cuda or (device is not None and t.device != device) or t.dim() != len(shape)
-            or not t.is_contiguous()):
+def _dense(t, dtype, shape, index, where: str):
+    """Pointer of a contiguous tensor of this type and shape (None: any extent) on GPU ``index``; refused otherwise."""
+    if t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
         _refuse(where)
-    for have, want in zip(t.shape, shape):
-        if want is not None and have != want:
-            _refuse(where)
+    have = t.shape
+    if have != shape and (len(have) != len(shape) or any(w is not None and n != w for n, w in zip(have, shape))):
+        _refuse(where)
     return t.data_ptr()
 
 
 def _rows(t, heads, rows, pool, where: str):
     """(pointer, rows, heads, row stride) of a [rows, heads, 128] bf16 tensor whose rows may lie apart."""
-    if t.dtype is not pool.bf16 or t.dim() != 3 or t.device != pool.device:
+    if t.dtype is not pool.bf16 or t.dim() != 3 or t.get_device() != pool.index:
         _refuse(where)
     n, h, d = t.shape
     row, head, one = t.stride()
@@ -265,9 +264,9 @@ class PagedBatch:
             _refuse(where)
         for t, shape in ((kv_len, (n,)), (q_start, (n + 1,)), (status, (1,))):
             if t is not None:
-                _dense(t, i32, shape, dev, where)
+                _dense(t, i32, shape, dev.index, where)
         self.page_table, self.kv_len, self.q_start, self.status = page_table, kv_len, q_start, status
-        self.device, self.n_seqs, self.max_kv = dev, n, max_kv
+        self.device, self.index, self.n_seqs, self.max_kv = dev, dev.index, n, max_kv
         self._c = _PagedBatch(_ptr(page_table), _ptr(kv_len), _ptr(q_start), _ptr(status), stride, n, max_q, max_kv)
         self._ref = ctypes.byref(self._c)
 
@@ -282,7 +281,7 @@ class PagedBatch:
 def paged_write(pool: PagePool, batch: PagedBatch, k, v, stream=None) -> None:
     """The chunk's K and V, [rows, kv_heads, 128] bf16, into the pages."""
     where = "rkv_paged_write"
-    if pool.device != batch.device:
+    if pool.index != batch.index:
         _refuse(where)
     kp, rows, _, ks = _rows(k, pool.kv_heads, None, pool, where)
     vp, _, _, vs = _rows(v, pool.kv_heads, rows, pool, where)
@@ -304,29 +303,29 @@ def paged_attention(pool: PagePool, batch: PagedBatch, q, out, causal: bool = Tr
     of every key, added up. ``workspace``: a uint8 tensor of ``paged_workspace_bytes`` (allocated on the
     call's stream if None)."""
     where = "rkv_paged_attention"
-    dev, torch = pool.device, pool.torch
-    if dev != batch.device:
+    index, torch = pool.index, pool.torch
+    if index != batch.index:
         _refuse(where)
     qp, rows, heads, qs = _rows(q, None, None, pool, where)
     op, _, _, os_ = _rows(out, heads, rows, pool, where)
     zp = wp = None
     width = 0
     if lse is not None:
-        zp = _dense(lse, torch.float32, (rows, heads), dev, where)
+        zp = _dense(lse, torch.float32, (rows, heads), index, where)
     if weight is not None:
-        wp = _dense(weight, torch.float32, (batch.n_seqs, pool.kv_heads, None), dev, where)
+        wp = _dense(weight, torch.float32, (batch.n_seqs, pool.kv_heads, None), index, where)
         width = weight.shape[2]
         if width < batch.max_kv:
             _refuse(where)  # here too: a tensor without elements has no address to refuse
     if workspace is None:
         size = paged_workspace_bytes(pool, batch, rows, heads, weight is not None)
         if stream is None:
-            stream = torch.cuda.current_stream(dev)
+            stream = torch.cuda.current_stream(index)
         elif isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream, dev) if stream else torch.cuda.default_stream(dev)
+            stream = torch.cuda.ExternalStream(stream, pool.device) if stream else torch.cuda.default_stream(index)
         with torch.cuda.stream(stream):
-            workspace = torch.empty(size, dtype=torch.uint8, device=dev)
-    sp = _dense(workspace, torch.uint8, (None,), dev, where)
+            workspace = torch.empty(size, dtype=torch.uint8, device=pool.device)
+    sp = _dense(workspace, torch.uint8, (None,), index, where)
     _launch(_lib.rkv_paged_attention, where, pool, stream, pool._ref, batch._ref, qp, heads, rows, qs, op, os_,
             1 if causal else 0, zp, wp, width, sp, workspace.shape[0])
 
@@ -337,12 +336,12 @@ def paged_evict(pool: PagePool, batch: PagedBatch, weight, keep: int, sinks: int
     in all, in their order. weight [n_seqs, kv_heads, tokens] fp32, kept [n_seqs, kv_heads, keep] int32 and
     kv_len_out [n_seqs] int32 (both written)."""
     where = "rkv_paged_evict"
-    dev, n, torch = pool.device, batch.n_seqs, pool.torch
-    if dev != batch.device:
+    index, n, torch = pool.index, batch.n_seqs, pool.torch
+    if index != batch.index:
         _refuse(where)
-    wp = _dense(weight, torch.float32, (n, pool.kv_heads, None), dev, where)
-    kp = _dense(kept, torch.int32, (n, pool.kv_heads, keep), dev, where)
-    lp = _dense(kv_len_out, torch.int32, (n,), dev, where)
+    wp = _dense(weight, torch.float32, (n, pool.kv_heads, None), index, where)
+    kp = _dense(kept, torch.int32, (n, pool.kv_heads, keep), index, where)
+    lp = _dense(kv_len_out, torch.int32, (n,), index, where)
     _launch(_lib.rkv_paged_evict, where, pool, stream, pool._ref, batch._ref, wp, weight.shape[2], keep, sinks,
             recent, kp, lp)
 

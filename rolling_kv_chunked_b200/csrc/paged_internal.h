@@ -1,5 +1,5 @@
 // Internal interface between the paged caches' host side (rkv_paged_host.cpp) and their kernels
-// (rkv_paged.cu, rkv_paged_decode.cu, rkv_paged_attention.cu). Not installed.
+// (rkv_paged.cu, rkv_paged_decode.cu, rkv_paged_attention.cu, rkv_paged_join.cu). Not installed.
 #pragma once
 
 #include "rkv_internal.h"
