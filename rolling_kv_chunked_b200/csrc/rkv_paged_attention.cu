@@ -27,6 +27,7 @@
 // bytes the tile holds there; V rows past the last visible token are left out of the product in
 // steps of 16 tokens, and zeroed within the last step, since 0 times a stale NaN would be NaN.
 // Every wait is bounded; on expiry the block reports, drains what it issued and returns.
+#include <algorithm>
 #include <mutex>
 
 #include "attention_tile.cuh"
@@ -73,9 +74,10 @@ constexpr uint32_t kIdescS = ptx::idesc_bf16_f32(kBM, kBN, false);
 constexpr uint32_t kIdescPV = ptx::idesc_bf16_f32(kBM, kHeadDim, true);
 
 // ---------------------------------------------------------------- the plan
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanNear = 1024;  // streams, and blocks of rows, that the plan holds in shared memory
 
 // Exclusive sum over the thread block, and its total.
+template <int kPlanThreads>
 __device__ __forceinline__ int plan_scan(int x, int* warp_sums, int& total) {
   const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5;
   int inc = x;
@@ -87,7 +89,7 @@ __device__ __forceinline__ int plan_scan(int x, int* warp_sums, int& total) {
   __syncthreads();
   if (lane == 31) warp_sums[wp] = inc;
   __syncthreads();
-  const int v = warp_sums[lane];
+  const int v = lane < kPlanThreads / 32 ? warp_sums[lane] : 0;
   total = __reduce_add_sync(0xffffffffu, v);
   return inc - x + __reduce_add_sync(0xffffffffu, lane < wp ? v : 0);
 }
@@ -97,20 +99,23 @@ __device__ __forceinline__ int last_at_most(const int* near, const int* far, int
   int lo = 0, hi = n;
   while (hi - lo > 1) {
     const int m = (lo + hi) >> 1;
-    const int v = n <= kPlanThreads ? near[m] : far[static_cast<long long>(m) * stride];
+    const int v = n <= kPlanNear ? near[m] : far[static_cast<long long>(m) * stride];
     if (v <= y) lo = m; else hi = m;
   }
   return lo;
 }
 
 // One thread block: the units of the batch and their key tiles, from the lengths on the device, and how
-// they are shared.
+// they are shared. 256 threads, unless there are more streams or blocks: its time is that of some ten barriers, and the
+// more warps the longer each takes (5 units of one tile: 16.1 us with 1024, 15.3 with 256).
+template <int kPlanThreads>
 __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_constant__ PagedAttnParams p) {
-  __shared__ int warp_sums[32];
-  __shared__ int sizes[2][32];
-  __shared__ int near_seq[kPlanThreads];        // first block of every stream, if there are that few
-  __shared__ int near_start[kPlanThreads + 1];  // first tile of every block
-  __shared__ int2 near_rows[kPlanThreads];      // its first row and tokens
+  constexpr int kPlanWarps = kPlanThreads / 32;
+  __shared__ int warp_sums[kPlanWarps];
+  __shared__ int sizes[2][kPlanWarps];
+  __shared__ int near_seq[kPlanNear];    // first block of every stream, if there are that few
+  __shared__ int near_start[kPlanNear];  // first tile of every block, if there are that few
+  __shared__ int2 near_rows[kPlanNear];  // its first row and tokens
   __shared__ int near_rest[kSmCount + 2];
   ptx::let_next_launch();
   ptx::wait_previous();
@@ -130,24 +135,26 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
         paged_report(w, kStatusLength);
     }
     int total;
-    const int first = blocks + plan_scan(c, warp_sums, total);
+    const int first = blocks + plan_scan<kPlanThreads>(c, warp_sums, total);
     if (s < w.n_seqs) p.seq_first[s] = first;
-    if (base == 0) near_seq[t] = first;
+    if (s < kPlanNear) near_seq[s] = first;
     blocks += total;
   }
   // row ranges that overlap (q_start decreases: reported above) may need more blocks than the list holds, or than
   // 31 bits count: then there is no work
   if (__syncthreads_or(falls)) blocks = 0;
   // for the weights: the streams with the longest chunks first, so that the last key tiles drawn are short work
-  if (p.order != nullptr && t < w.n_seqs) {
+  if (p.order != nullptr) {
     auto length = [&](int s) { return (s + 1 < w.n_seqs ? near_seq[s + 1] : blocks) - near_seq[s]; };
-    const int mine = length(t);
-    int rank = 0;
-    for (int s = 0; s < w.n_seqs; ++s) {
-      const int x = length(s);
-      rank += x > mine || (x == mine && s < t);
+    for (int i = t; i < w.n_seqs; i += kPlanThreads) {
+      const int mine = length(i);
+      int rank = 0;
+      for (int s = 0; s < w.n_seqs; ++s) {
+        const int x = length(s);
+        rank += x > mine || (x == mine && s < i);
+      }
+      p.order[rank] = i;
     }
-    p.order[rank] = t;
   }
   int tiles = 0, most = 0, least = 1 << 30;
   for (int base = 0; base < blocks; base += kPlanThreads) {
@@ -156,7 +163,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
     if (b < blocks) {
       const int s = last_at_most(near_seq, p.seq_first, 1, w.n_seqs, b);
       const PagedSeq q = paged_seq(w, s);
-      const int i0 = (b - (w.n_seqs <= kPlanThreads ? near_seq[s] : p.seq_first[s])) * p.block_tokens;
+      const int i0 = (b - (w.n_seqs <= kPlanNear ? near_seq[s] : p.seq_first[s])) * p.block_tokens;
       k.row0 = q.q0 + i0;
       k.cnt = min(p.block_tokens, q.n_q - i0);
       k.keys = p.causal ? max(0, q.kv - q.n_q + i0 + k.cnt) : q.kv;
@@ -167,12 +174,11 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
       least = min(least, k.tiles);
     }
     int total;
-    k.start = tiles + plan_scan(k.tiles, warp_sums, total);
+    k.start = tiles + plan_scan<kPlanThreads>(k.tiles, warp_sums, total);
     if (b < blocks) p.blocks[b] = k;
-    if (base == 0) {
-      near_start[t] = k.start;
-      near_rows[t] = make_int2(k.row0, k.cnt);
-      if (t == kPlanThreads - 1) near_start[kPlanThreads] = k.start + k.tiles;
+    if (b < blocks && b < kPlanNear) {
+      near_start[b] = k.start;
+      near_rows[b] = make_int2(k.row0, k.cnt);
     }
     tiles += total;
   }
@@ -184,12 +190,12 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
     sizes[1][t >> 5] = least;
   }
   __syncthreads();
-  most = __reduce_max_sync(0xffffffffu, sizes[0][t & 31]);
-  least = __reduce_min_sync(0xffffffffu, sizes[1][t & 31]);
+  most = __reduce_max_sync(0xffffffffu, sizes[0][t % kPlanWarps]);
+  least = __reduce_min_sync(0xffffffffu, sizes[1][t % kPlanWarps]);
   auto tiles_of = [&](int b) {
-    return blocks <= kPlanThreads ? (b + 1 < blocks ? near_start[b + 1] : tiles) - near_start[b] : p.blocks[b].tiles;
+    return blocks <= kPlanNear ? (b + 1 < blocks ? near_start[b + 1] : tiles) - near_start[b] : p.blocks[b].tiles;
   };
-  auto start_of = [&](int b) { return blocks <= kPlanThreads ? near_start[b] : p.blocks[b].start; };
+  auto start_of = [&](int b) { return blocks <= kPlanNear ? near_start[b] : p.blocks[b].start; };
 
   const long long units = static_cast<long long>(blocks) * w.kv_heads;
   const long long all = static_cast<long long>(tiles) * w.kv_heads;
@@ -199,12 +205,12 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
   int n = 0;  // thread i < n_tail: tiles of the i-th of them
   if (t < n_tail) n = tiles_of(static_cast<int>(first + t - quotient(first + t, blocks) * blocks));
   int tail_tiles;
-  plan_scan(n, warp_sums, tail_tiles);
+  plan_scan<kPlanThreads>(n, warp_sums, tail_tiles);
   const int quota = (tail_tiles + kSmCount - 1) / kSmCount;
   // in step: sizes within an eighth of each other
   const bool in_step = blocks > 0 && least >= most - most / 8;
   int rest_tiles;
-  const int rest = plan_scan(max(0, n - quota), warp_sums, rest_tiles);
+  const int rest = plan_scan<kPlanThreads>(max(0, n - quota), warp_sums, rest_tiles);
   if (t <= n_tail) out->rest[t] = near_rest[t] = rest;
   if (t == 0) *p.ticket = 0;
   // in a row: shares down to one tile, since idle SMs cost more than the merge (6 units of 8 to 11 tiles: 16 us; 25
@@ -265,8 +271,8 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
     }
   }
   if (join.parts > 0) {
-    join.row0 = blocks <= kPlanThreads ? near_rows[joined].x : p.blocks[joined].row0;
-    join.cnt = blocks <= kPlanThreads ? near_rows[joined].y : p.blocks[joined].cnt;
+    join.row0 = blocks <= kPlanNear ? near_rows[joined].x : p.blocks[joined].row0;
+    join.cnt = blocks <= kPlanNear ? near_rows[joined].y : p.blocks[joined].cnt;
   }
   out->share[t] = mine;
   p.joins[t] = join;
@@ -1092,7 +1098,8 @@ cudaError_t launch_paged_chunk(const CUtensorMap& tm_q, const CUtensorMap& tm_k,
                                const PagedAttnParams& p, cudaStream_t stream) {
   cudaError_t err = configure();
   if (err != cudaSuccess) return err;
-  err = launch_after(paged_plan_kernel, 1, kPlanThreads, 0, stream, p);
+  const bool small = std::max(p.view.n_seqs, p.n_blocks) <= 256;
+  err = launch_after(small ? paged_plan_kernel<256> : paged_plan_kernel<1024>, 1, small ? 256 : 1024, 0, stream, p);
   if (err == cudaSuccess)
     err = launch_after(paged_chunk_kernel, kSmCount, kThreads, kSmemBytes, stream, tm_q, tm_k, tm_v, p);
   return err;
