@@ -83,6 +83,10 @@ __device__ __forceinline__ long long paged_offset(const PagedView& w, int id, in
          (static_cast<long long>(h) * (1 << w.page_shift) + slot) * kHeadDim;
 }
 
+// A part of the chunk form: float4 number `col` (of 32) of row `row`. Eight rows lie side by side, so that a thread per
+// row writes, and a thread per row and float4 reads, whole lines.
+__device__ __forceinline__ int paged_part_place(int row, int col) { return ((row >> 3) * 32 + col) * 8 + (row & 7); }
+
 // x / y where both nearly always fit 32 bits (a 64-bit division is some 100 instructions).
 __device__ __forceinline__ long long quotient(long long x, long long y) {
   return ((x | y) >> 32) == 0 ? static_cast<long long>(static_cast<unsigned>(x) / static_cast<unsigned>(y)) : x / y;

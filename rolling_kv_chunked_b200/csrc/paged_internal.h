@@ -97,7 +97,7 @@ struct PagedAttnParams {
   // workspace
   float* lse2;      // [n_rows][q_heads], log2; null when no weight is wanted
   float* part;      // unnormalised sums of p v of cut units: [4 * kSmCount][slot_rows][128] (single-token
-                    // form) or [2 * kSmCount][kPagedPartRows][128]
+                    // form) or [2 * kSmCount][kPagedPartRows * 128] (paged_part_place)
   float2* part_ml;  // the same rows: reference (log2) and sum of p
   PagedJoin* joins;    // [n_joins], an entry per thread block of the attention
   PagedBlock* blocks;  // chunk form: [n_blocks]
