@@ -493,6 +493,23 @@ __device__ __forceinline__ void softmax_tile(bool first, int valid, uint32_t tS,
   }
 }
 
+// a[v] of lane q of four becomes a[q] of lane v.
+__device__ __forceinline__ void swap_lanes(uint4& a, uint4& b, int bit, bool upper) {
+  uint4 x = upper ? a : b;
+  x.x = __shfl_xor_sync(0xffffffffu, x.x, bit);
+  x.y = __shfl_xor_sync(0xffffffffu, x.y, bit);
+  x.z = __shfl_xor_sync(0xffffffffu, x.z, bit);
+  x.w = __shfl_xor_sync(0xffffffffu, x.w, bit);
+  a = upper ? x : a;
+  b = upper ? b : x;
+}
+__device__ __forceinline__ void transpose4(uint4 (&a)[4], int lane) {
+  swap_lanes(a[0], a[1], 1, lane & 1);
+  swap_lanes(a[2], a[3], 1, lane & 1);
+  swap_lanes(a[0], a[2], 2, lane & 2);
+  swap_lanes(a[1], a[3], 2, lane & 2);
+}
+
 __global__ void __launch_bounds__(kThreads, 1)
     paged_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ PagedAttnParams p) {
@@ -781,6 +798,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float inv = l == 0.f ? 0.f : 1.0f / l;  // a row that saw nothing: its accumulator may hold anything
       const int part_row = (u.two ? wg * kBM : 0) + r;
       float4* part = reinterpret_cast<float4*>(p.part) + static_cast<long long>(u.slot) * kPagedPartRows * (kHeadDim / 4);
+      // where this lane writes its 16 bytes of each of the rows of its group of four lanes
+      uint16_t* to[4];
+      const unsigned live_rows = __ballot_sync(0xffffffffu, live) >> (lane & ~3);
+      {
+        const unsigned long long mine = reinterpret_cast<unsigned long long>(p.out + row * p.out_stride + head * kHeadDim);
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          to[v] = reinterpret_cast<uint16_t*>(__shfl_sync(0xffffffffu, mine, (lane & ~3) + v)) + (lane & 3) * 8;
+      }
 #pragma unroll 1
       for (int c = u.two ? 0 : 2 * wg; ok && c < (u.two ? 4 : 2 * wg + 2); ++c) {
         uint32_t rr[32];
@@ -793,16 +819,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) x[i] += __uint_as_float(rr[i]) * f1;
         }
-        if (!live) continue;
         if (whole) {
-          uint32_t ob[16];
+          uint4 ob[4];
+          uint32_t* o32 = reinterpret_cast<uint32_t*>(ob);
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            ob[i] = l != 0.f ? pack_bf16x2(x[2 * i] * inv, x[2 * i + 1] * inv) : 0u;
-          uint4* dst = reinterpret_cast<uint4*>(p.out + row * p.out_stride + head * kHeadDim + 32 * c);
+            o32[i] = l != 0.f ? pack_bf16x2(x[2 * i] * inv, x[2 * i + 1] * inv) : 0u;
+          // a row's 64 bytes by four lanes at once instead of by one lane piece after piece (3000 streams of 20 tokens:
+          // 199 us instead of 205; the code costs the long units' loop up to a hundredth)
+          transpose4(ob, lane);
 #pragma unroll
-          for (int v = 0; v < 4; ++v) dst[v] = make_uint4(ob[4 * v], ob[4 * v + 1], ob[4 * v + 2], ob[4 * v + 3]);
-        } else {
+          for (int v = 0; v < 4; ++v)
+            if (live_rows >> v & 1u) *reinterpret_cast<uint4*>(to[v] + 32 * c) = ob[v];
+        } else if (live) {
           // whole lines: 512 bytes of one row per thread, the rows' one after the other, made this 6 us of a unit
 #pragma unroll
           for (int v = 0; v < 8; ++v)
