@@ -537,7 +537,8 @@ __global__ void __launch_bounds__(kTokenWeightThreads)
     const long long rh = static_cast<long long>(q.q0 + t) * p.q_heads + h * p.group;
 #pragma unroll 4
     for (int g = 0; g < p.group; ++g) {
-      const float z = p.lse2[rh + g];
+      // a row that sees no key has z = -infinity and nothing but scores of -infinity: +infinity gives its keys 0
+      const float lse = p.lse2[rh + g], z = lse == -INFINITY ? INFINITY : lse;
       const float* sc = p.scores + (rh + g) * p.score_stride;
 #pragma unroll
       for (int k = 0; k < kTokenWeightKeys; ++k) {

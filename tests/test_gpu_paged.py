@@ -705,3 +705,23 @@ def test_poll_follows_its_stream():
         for _ in range(50):
             c.attend()
             assert c.batch.poll() == rkv.ERR_PAGE
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("kvs,qs,hq,hk", [
+    ([2], [3], 1, 1),
+    ([3, 40], [5, 4], 4, 2),               # 10 rows of a KV head: scores kept
+    ([9, 2, 100], [16, 3, 1], 2, 2),       # 16
+    ([0, 1, 700], [4, 4, 4], 12, 3),       # 16, a stream without tokens
+    ([3, 40], [20, 11], 2, 2),             # 20: scores formed again
+    ([5, 3000], [9, 16], 4, 2),            # 32
+    ([260, 40], [300, 7], 4, 2),           # tiles of 128 rows
+])
+def test_weights_of_rows_that_see_nothing(kvs, qs, hq, hk, causal):
+    """Chunks longer than the cache: their first rows see no key and give none weight, twice in a row."""
+    c = Cache(40, kvs, qs, hq, hk, 16)
+    weight = torch.rand((len(kvs), hk, c.max_kv + 2), device="cuda")
+    for _ in range(2):
+        old = weight.clone()
+        out, z = c.attend(causal, weight=weight)
+        c.check(out, z, causal, weight, old)
