@@ -370,7 +370,8 @@ typedef struct {
 } rkv_page_pool;
 
 /* The streams of one step; every layer's calls of the step can share it. Device pointers
- *  except where noted. table_stride * page_tokens must reach max_kv. */
+ *  except where noted. Every row of page_table has entries for max_kv tokens: table_stride *
+ *  page_tokens must reach max_kv (where the rows are a slice of wider ones, so must their own entries). */
 typedef struct {
   const int* page_table; /* [n_seqs][table_stride]: page ids in logical order          */
   const int* kv_len;     /* [n_seqs]                                                   */

@@ -208,6 +208,13 @@ def _rows(t, heads, rows, pool, where: str):
     return t.data_ptr(), n, h, row if n > 1 else h * 128
 
 
+def _pair(pool, batch, where: str) -> None:
+    """Pool and batch fit: the same GPU, and page lists whose columns reach max_kv. (The library sees the lists' stride
+    only, and a column slice's stride counts columns that are not its own.)"""
+    if pool.index != batch.index or batch.width * pool.page_tokens < batch.max_kv:
+        _refuse(where)
+
+
 def _launch(fn, where: str, pool, stream, *args) -> None:
     """Call with the tensors' device current and, unless a stream is given, on its current stream."""
     torch, index = pool.torch, pool.index
@@ -240,7 +247,7 @@ class PagePool:
                 _refuse(where)
         if n > 1 and k.stride(0) != v.stride(0):
             _refuse(where)
-        self.k, self.v, self.device, self.kv_heads = k, v, k.device, h
+        self.k, self.v, self.device, self.kv_heads, self.page_tokens = k, v, k.device, h, p
         self.torch, self.index, self.bf16 = torch, k.device.index, torch.bfloat16
         self._c = _PagePool(k.data_ptr(), v.data_ptr(), k.stride(0) if n > 1 else h * p * 128, n, h, p)
         self._ref = ctypes.byref(self._c)
@@ -249,8 +256,8 @@ class PagePool:
 class PagedBatch:
     """The streams of one step: page_table [n_seqs, pages] int32, kv_len [n_seqs] int32, q_start
     [n_seqs + 1] int32 (None for eviction only), all on the GPU, and host bounds of chunk rows and
-    cached tokens per stream. ``status``: one zeroed int32 on the GPU that collects errors
-    (``poll``); without it they are not reported. Layers can share one."""
+    cached tokens per stream (page_table has columns for max_kv tokens). ``status``: one zeroed int32
+    on the GPU that collects errors (``poll``); without it they are not reported. Layers can share one."""
 
     def __init__(self, page_table, kv_len, q_start, max_q: int, max_kv: int, status=None):
         where = "PagedBatch"
@@ -266,7 +273,7 @@ class PagedBatch:
             if t is not None:
                 _dense(t, i32, shape, dev.index, where)
         self.page_table, self.kv_len, self.q_start, self.status = page_table, kv_len, q_start, status
-        self.device, self.index, self.n_seqs, self.max_kv = dev, dev.index, n, max_kv
+        self.device, self.index, self.n_seqs, self.width, self.max_kv = dev, dev.index, n, width, max_kv
         self._c = _PagedBatch(_ptr(page_table), _ptr(kv_len), _ptr(q_start), _ptr(status), stride, n, max_q, max_kv)
         self._ref = ctypes.byref(self._c)
 
@@ -281,8 +288,7 @@ class PagedBatch:
 def paged_write(pool: PagePool, batch: PagedBatch, k, v, stream=None) -> None:
     """The chunk's K and V, [rows, kv_heads, 128] bf16, into the pages."""
     where = "rkv_paged_write"
-    if pool.index != batch.index:
-        _refuse(where)
+    _pair(pool, batch, where)
     kp, rows, _, ks = _rows(k, pool.kv_heads, None, pool, where)
     vp, _, _, vs = _rows(v, pool.kv_heads, rows, pool, where)
     _launch(_lib.rkv_paged_write, where, pool, stream, pool._ref, batch._ref, kp, vp, rows, ks, vs)
@@ -290,6 +296,7 @@ def paged_write(pool: PagePool, batch: PagedBatch, k, v, stream=None) -> None:
 
 def paged_workspace_bytes(pool: PagePool, batch: PagedBatch, rows: int, q_heads: int, weight: bool = False) -> int:
     """Bytes of workspace that ``paged_attention`` needs for a chunk tensor of ``rows`` rows."""
+    _pair(pool, batch, "rkv_paged_workspace")
     n = _c_ll(0)
     _check(_lib.rkv_paged_workspace(pool._ref, batch._ref, q_heads, rows, int(bool(weight)), ctypes.byref(n)),
            "rkv_paged_workspace")
@@ -304,8 +311,7 @@ def paged_attention(pool: PagePool, batch: PagedBatch, q, out, causal: bool = Tr
     call's stream if None)."""
     where = "rkv_paged_attention"
     index, torch = pool.index, pool.torch
-    if index != batch.index:
-        _refuse(where)
+    _pair(pool, batch, where)
     qp, rows, heads, qs = _rows(q, None, None, pool, where)
     op, _, _, os_ = _rows(out, heads, rows, pool, where)
     zp = wp = None
@@ -337,8 +343,7 @@ def paged_evict(pool: PagePool, batch: PagedBatch, weight, keep: int, sinks: int
     kv_len_out [n_seqs] int32 (both written)."""
     where = "rkv_paged_evict"
     index, n, torch = pool.index, batch.n_seqs, pool.torch
-    if index != batch.index:
-        _refuse(where)
+    _pair(pool, batch, where)
     wp = _dense(weight, torch.float32, (n, pool.kv_heads, None), index, where)
     kp = _dense(kept, torch.int32, (n, pool.kv_heads, keep), index, where)
     lp = _dense(kv_len_out, torch.int32, (n,), index, where)

@@ -725,3 +725,28 @@ def test_weights_of_rows_that_see_nothing(kvs, qs, hq, hk, causal):
         old = weight.clone()
         out, z = c.attend(causal, weight=weight)
         c.check(out, z, causal, weight, old)
+
+
+def test_a_page_table_too_narrow_for_the_bound_is_refused():
+    """A column slice of a wider table: its stride would reach max_kv, its columns do not."""
+    c = Cache(41, [30, 20], [1, 1], 4, 2, 16)
+    wide = torch.zeros((2, 5), dtype=torch.int32, device="cuda")
+    wide[:, :2] = c.table
+    weight = torch.zeros((2, 2, 64), device="cuda")
+    kept = torch.empty((2, 2, 8), dtype=torch.int32, device="cuda")
+    k = c.normal(c.rows, 2, 128)
+    out = torch.empty_like(c.q)
+
+    def calls(b):
+        yield lambda: rkv.paged_write(c.pool, b, k, k)
+        yield lambda: rkv.paged_attention(c.pool, b, c.q, out)
+        yield lambda: rkv.paged_workspace_bytes(c.pool, b, c.rows, 4)
+        yield lambda: rkv.paged_evict(c.pool, b, weight, 8, 1, 1, kept, torch.empty_like(c.kv_len))
+
+    for call in calls(rkv.PagedBatch(wide[:, :2], c.kv_len, c.q_start, 1, 33)):
+        with pytest.raises(rkv.RkvError) as e:
+            call()
+        assert e.value.code == rkv.ERR_ARG
+    for call in calls(rkv.PagedBatch(wide[:, :2], c.kv_len, c.q_start, 1, 32)):  # all of the columns
+        call()
+    torch.cuda.synchronize()
