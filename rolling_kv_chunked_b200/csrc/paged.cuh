@@ -54,8 +54,9 @@ __device__ __forceinline__ int paged_seq_of_row(const PagedView& w, int row) {
 }
 
 struct PagedSeq {
-  int q0, n_q, kv;  // first chunk row, chunk rows, cached tokens
+  int q0, n_q, kv;  // first chunk row, chunk rows (if ok), cached tokens
   bool ok;
+  bool falls;  // its row range ends before it begins
 };
 
 // The lengths of stream s, checked against the batch's bounds.
@@ -65,7 +66,8 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedView& w, int s) {
   const int q1 = __ldg(w.q_start + s + 1);
   r.kv = __ldg(w.kv_len + s);
   r.ok = r.q0 >= 0 && q1 >= r.q0 && q1 <= w.n_rows && q1 - r.q0 <= w.max_q && r.kv >= 0 && r.kv <= w.max_kv;
-  r.n_q = q1 - r.q0;
+  r.falls = q1 < r.q0;
+  r.n_q = r.ok ? q1 - r.q0 : 0;  // the difference of any two ints may not fit one
   return r;
 }
 

@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const __grid_c
     int c = 0;
     if (s < w.n_seqs) {
       const PagedSeq q = paged_seq(w, s);
-      falls |= q.n_q < 0;
+      falls |= q.falls;
       if (q.ok)
         c = (q.n_q + p.block_tokens - 1) / p.block_tokens;
       else

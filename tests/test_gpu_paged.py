@@ -750,3 +750,22 @@ def test_a_page_table_too_narrow_for_the_bound_is_refused():
     for call in calls(rkv.PagedBatch(wide[:, :2], c.kv_len, c.q_start, 1, 32)):  # all of the columns
         call()
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("hq,n", [(4, 8), (8, 16), (128, 1000)])  # 16 and 32 rows of a KV head, and blocks of two tokens
+def test_row_ranges_whose_differences_pass_31_bits(hq, n):
+    """q_start falls by so much that every difference wraps to a positive number, and the same rows come twice: reported,
+    and neither rows outside the streams' nor anything behind the workspace is touched."""
+    c = Cache(46, [1000] * 10, [n] + [0] * 9, hq, 2 if hq < 128 else 1, 16, max_q=n)
+    far = (1 << 31) - 1
+    c.q_start.copy_(torch.tensor([0, n, far, -far - 1, -1] * 2 + [0], dtype=torch.int64).to(torch.int32))
+    weight = torch.ones((10, c.hk, 1003), device="cuda")
+    size = rkv.paged_workspace_bytes(c.pool, c.batch, c.rows + c.spare, hq, True)
+    ws = torch.full((size + 65536,), 85, dtype=torch.uint8, device="cuda")
+    out, z = c.attend(weight=weight, workspace=ws)
+    assert c.batch.poll() == rkv.ERR_PAGE
+    assert (ws[size:] == 85).all()
+    assert (out[n:] == 7.0).all() and (z[n:] == 7.0).all() and (weight[:, :, 1000:] == 1).all()
+    k = c.normal(c.rows + c.spare, c.hk, 128)
+    rkv.paged_write(c.pool, c.batch, k, k)
+    assert c.batch.poll() == rkv.ERR_PAGE
