@@ -10,6 +10,8 @@ namespace rkv {
 
 // Launch a kernel that may be set up while the stream's previous one still runs; it waits for that one
 // itself (ptx::wait_previous, in every thread block, before it touches memory).
+// What it reads may still be written while it is resident, so no load of it may be one of read-only data
+// (__ldg, which holds for memory that no one writes during the whole kernel): plain loads, after the wait.
 template <typename... P, typename... A>
 cudaError_t launch_after(void (*kernel)(P...), dim3 grid, unsigned block, size_t smem, cudaStream_t stream,
                          A&&... args) {
@@ -39,7 +41,7 @@ __device__ __forceinline__ int paged_seq_of_row(const PagedView& w, int row) {
   while (hi > lo) {
     const int step = (hi - lo + 31) / 32;
     const int i = lo + lane * step;
-    const bool le = i < hi && __ldg(w.q_start + i) <= row;
+    const bool le = i < hi && w.q_start[i] <= row;
     const int c = __popc(__ballot_sync(0xffffffffu, le));
     if (c == 0) {
       hi = lo;
@@ -62,9 +64,9 @@ struct PagedSeq {
 // The lengths of stream s, checked against the batch's bounds.
 __device__ __forceinline__ PagedSeq paged_seq(const PagedView& w, int s) {
   PagedSeq r;
-  r.q0 = __ldg(w.q_start + s);
-  const int q1 = __ldg(w.q_start + s + 1);
-  r.kv = __ldg(w.kv_len + s);
+  r.q0 = w.q_start[s];
+  const int q1 = w.q_start[s + 1];
+  r.kv = w.kv_len[s];
   r.ok = r.q0 >= 0 && q1 >= r.q0 && q1 <= w.n_rows && q1 - r.q0 <= w.max_q && r.kv >= 0 && r.kv <= w.max_kv;
   r.falls = q1 < r.q0;
   r.n_q = r.ok ? q1 - r.q0 : 0;  // the difference of any two ints may not fit one
@@ -73,7 +75,7 @@ __device__ __forceinline__ PagedSeq paged_seq(const PagedView& w, int s) {
 
 // Page id at place `i` of stream s's list, or -1 (reported) if it is not a page of the pool.
 __device__ __forceinline__ int paged_id(const PagedView& w, int s, int i) {
-  const int id = __ldg(w.table + static_cast<long long>(s) * w.table_stride + i);
+  const int id = w.table[static_cast<long long>(s) * w.table_stride + i];
   if (static_cast<unsigned>(id) < static_cast<unsigned>(w.n_pages)) return id;
   paged_report(w, kStatusPage);
   return -1;

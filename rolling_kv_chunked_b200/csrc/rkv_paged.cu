@@ -42,8 +42,8 @@ __global__ void __launch_bounds__(kWriteWarps * 32) paged_write_kernel(const __g
     for (int i = 0; i < kWriteBatch; ++i) {
       const int h = h0 + 2 * i;
       if (h < w.kv_heads) {
-        kx[i] = __ldg(reinterpret_cast<const uint4*>(p.k + row * p.k_stride + h * kHeadDim + c));
-        vx[i] = __ldg(reinterpret_cast<const uint4*>(p.v + row * p.v_stride + h * kHeadDim + c));
+        kx[i] = *reinterpret_cast<const uint4*>(p.k + row * p.k_stride + h * kHeadDim + c);
+        vx[i] = *reinterpret_cast<const uint4*>(p.v + row * p.v_stride + h * kHeadDim + c);
       }
     }
 #pragma unroll
@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(const __grid_
   const int s = sh / w.kv_heads;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   ptx::wait_previous();
-  const int n = __ldg(w.kv_len + s);
+  const int n = w.kv_len[s];
   int* kept = p.kept + static_cast<long long>(sh) * p.keep;
   const bool bad = n < 0 || n > w.max_kv;
   if (bad || n <= p.keep) {  // the same in the whole cluster
@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(const __grid_
 #pragma unroll
     for (int k = 0; k < kHeldKeys; ++k) {
       const int i = i0 + 32 * k + lane;
-      held[k] = i < i1 ? weight_key(__ldg(wt + i)) : 0u;
+      held[k] = i < i1 ? weight_key(wt[i]) : 0u;
     }
   }
   // f(token, its key) for this lane's tokens, 32 tokens of the run at a time, in order
@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(kSelThreads) paged_select_kernel(const __grid_
       }
     } else {
 #pragma unroll 8
-      for (int i = i0; i < i1; i += 32) f(i + lane, i + lane < i1 ? weight_key(__ldg(wt + i + lane)) : 0u);
+      for (int i = i0; i < i1; i += 32) f(i + lane, i + lane < i1 ? weight_key(wt[i + lane]) : 0u);
     }
   };
   unsigned prefix = 0, mask = 0;
@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(kMoveThreads) paged_move_kernel(const __grid_c
   // the list's raw entry (-1 where there is no token): checked where it is used, a whole tile after
   // its load was issued
   const int* table = w.table + static_cast<long long>(s) * w.table_stride;
-  auto page = [&](int j) { return j >= 0 ? __ldg(table + (j >> w.page_shift)) : -1; };
+  auto page = [&](int j) { return j >= 0 ? table[j >> w.page_shift] : -1; };
   auto checked = [&](int id, bool live) {
     if (static_cast<unsigned>(id) < static_cast<unsigned>(w.n_pages)) return id;
     if (live) paged_report(w, kStatusPage);

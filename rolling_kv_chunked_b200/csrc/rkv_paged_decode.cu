@@ -128,8 +128,8 @@ __device__ __forceinline__ void token_unit(const PagedAttnParams& p, const Token
     const uint16_t* src = p.q + (q.q0 + (live ? tok : 0)) * p.q_stride + (u.h * p.group + r - tok * p.group) * kHeadDim;
 #pragma unroll
     for (int kk = 0; kk < 8; ++kk) {
-      qa[kk][e] = live ? __ldg(reinterpret_cast<const uint32_t*>(src + kk * 16 + cq)) : 0u;
-      qa[kk][2 + e] = live ? __ldg(reinterpret_cast<const uint32_t*>(src + kk * 16 + 8 + cq)) : 0u;
+      qa[kk][e] = live ? *reinterpret_cast<const uint32_t*>(src + kk * 16 + cq) : 0u;
+      qa[kk][2 + e] = live ? *reinterpret_cast<const uint32_t*>(src + kk * 16 + 8 + cq) : 0u;
     }
   }
   // the last place each row sees

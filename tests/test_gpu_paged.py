@@ -769,3 +769,45 @@ def test_row_ranges_whose_differences_pass_31_bits(hq, n):
     k = c.normal(c.rows + c.spare, c.hk, 128)
     rkv.paged_write(c.pool, c.batch, k, k)
     assert c.batch.poll() == rkv.ERR_PAGE
+
+
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("qs", [[1, 1, 1], [5, 2, 3], [9, 30, 16], [70, 140, 1]])
+def test_calls_that_feed_each_other_without_a_pause(qs, captured):
+    """Each call reads what the one before it wrote (queries, weights, pages), the launches overlapping: the same
+    bits as with every call waited for."""
+    results = []
+    for paused in (True, False):
+        c = Cache(43, [900, 1500, 333], qs, 4, 2, 16)
+        weight = torch.rand((3, 2, c.max_kv), generator=c.g, device="cuda")
+        bufs = [c.q.clone(), torch.zeros_like(c.q), torch.zeros_like(c.q)]
+        kept = torch.empty((3, 2, 300), dtype=torch.int32, device="cuda")
+        new_len = torch.empty(3, dtype=torch.int32, device="cuda")
+        ws = torch.empty(rkv.paged_workspace_bytes(c.pool, c.batch, c.q.shape[0], 4, True), dtype=torch.uint8, device="cuda")
+
+        def steps():
+            for i in range(12):
+                a, b = bufs[i % 3], bufs[(i + 1) % 3]
+                for call in (lambda: rkv.paged_attention(c.pool, c.batch, a, b, weight=weight, workspace=ws),
+                             lambda: rkv.paged_write(c.pool, c.batch, b[:, :2], b[:, 2:]),
+                             lambda: rkv.paged_evict(c.pool, c.batch, weight, 300, 2, 100, kept, new_len)):
+                    call()
+                    if paused:
+                        torch.cuda.synchronize()
+
+        torch.cuda.synchronize()
+        if captured and not paused:
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                steps()
+            for _ in range(4):
+                graph.replay()
+        else:
+            for _ in range(4):
+                steps()
+        torch.cuda.synchronize()
+        assert c.batch.poll() == rkv.OK
+        results.append([t.view(torch.int16 if t.dtype == torch.bfloat16 else torch.int32).clone()
+                        for t in (c.k, c.v, weight, kept, *(b[:c.rows] for b in bufs))])
+    for x, y in zip(*results):
+        assert torch.equal(x, y)
