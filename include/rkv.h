@@ -345,8 +345,10 @@ int rkv_copy_heads(const rkv_head_copy* runs, int n_runs, int n_heads, void* str
  * before the write); positions are places in the stream's page list.
  *
  * Every stream s has kv_len[s] cached tokens, its chunk's own included, and the chunk's n_q =
- * q_start[s+1] - q_start[s] rows stand at places kv_len[s] - n_q .. kv_len[s] - 1. Streams
- * without rows are left alone. Rows of the chunk tensors outside
+ * q_start[s+1] - q_start[s] rows stand at places kv_len[s] - n_q .. kv_len[s] - 1. A chunk may be
+ * longer than kv_len[s]: rows at places before the first are not cached, which is no error, and
+ * as queries they see what their place says (with causal nothing). Streams without rows are
+ * left alone. Rows of the chunk tensors outside
  * [q_start[0], q_start[n_seqs]) are neither read for a result nor written.
  *
  * What a device array holds is checked on the device: a length outside its bound (0 <=
@@ -385,7 +387,7 @@ typedef struct {
 
 /*
  * rkv_paged_write - the chunk's K and V into the pages: row i of stream s to place
- *  kv_len[s] - n_q + i. A bit copy. k, v: [n_rows, kv_heads, 128] bf16, 16-byte aligned,
+ *  kv_len[s] - n_q + i; a row whose place would be negative is left out. A bit copy. k, v: [n_rows, kv_heads, 128] bf16, 16-byte aligned,
  *  k_stride / v_stride elements from one row to the next (multiples of 8, at least
  *  kv_heads * 128). A page listed twice under the written places holds one of the two writes.
  *  Errors: RKV_ERR_ARG, RKV_ERR_UNSUPPORTED, RKV_ERR_CUDA.

@@ -28,10 +28,11 @@ __global__ void __launch_bounds__(kWriteWarps * 32) paged_write_kernel(const __g
   const int lane = threadIdx.x & 31;
   const int at = row - q.q0;  // the search finds another stream's range where q_start decreases
   const int pos = q.kv - q.n_q + at;
-  if (!q.ok || at < 0 || at >= q.n_q || pos < 0) {
+  if (!q.ok || at < 0 || at >= q.n_q) {
     if (lane == 0) paged_report(w, kStatusLength);
     return;
   }
+  if (pos < 0) return;  // a chunk longer than its stream: this row has no place
   const int id = paged_id(w, s, pos >> w.page_shift);
   if (id < 0) return;
   const int slot = pos & ((1 << w.page_shift) - 1);

@@ -811,3 +811,22 @@ def test_calls_that_feed_each_other_without_a_pause(qs, captured):
                         for t in (c.k, c.v, weight, kept, *(b[:c.rows] for b in bufs))])
     for x, y in zip(*results):
         assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("kvs,qs", [([2], [3]), ([3, 40, 0], [5, 4, 2]), ([130, 20], [140, 33])])
+def test_write_of_a_chunk_longer_than_its_stream(kvs, qs):
+    """Rows at places before the first are left out, the others written, and none of it is an error: as in the
+    attention, where those rows see nothing."""
+    c = Cache(42, kvs, qs, 2, 2, 16)
+    want_k, want_v = c.k.clone(), c.v.clone()
+    k, v = c.normal(c.rows, 2, 128), c.normal(c.rows, 2, 128)
+    rkv.paged_write(c.pool, c.batch, k, v)
+    for s, (n, m) in enumerate(zip(kvs, qs)):
+        a, _ = c.rows_of(s)
+        for i in range(max(0, m - n), m):
+            pos = n - m + i
+            for pages, x in ((want_k, k), (want_v, v)):
+                pages[c.table[s, pos // 16].long(), :, pos % 16] = x[a + i]
+    assert torch.equal(c.k.view(torch.int16), want_k.view(torch.int16))
+    assert torch.equal(c.v.view(torch.int16), want_v.view(torch.int16))
+    assert c.batch.poll() == rkv.OK
