@@ -422,6 +422,12 @@ int rkv_paged_attention(const rkv_page_pool* pool, const rkv_paged_batch* batch,
 
 /* rkv_paged_workspace - bytes of workspace that rkv_paged_attention needs for these host
  *  values (device arrays are not read; it needs no GPU). with_weight: weight will be passed.
+ *  Partial results: 5 MB for at most 16 rows per stream and KV head (max_q times the heads of a
+ *  group), 10 MB for at most 32, else 40 MB and a little for every stream and block of rows. With
+ *  weights 4 bytes per row and query head, and for at most 16 rows per stream and KV head the
+ *  scores: 4 * n_rows * q_heads * max_kv bytes (max_kv in steps of 64) if that is at most 2^32.
+ *  Past that the weights take more time instead (K is read again); a max_kv close to the lengths
+ *  avoids both.
  *  Errors: RKV_ERR_ARG, RKV_ERR_UNSUPPORTED. */
 int rkv_paged_workspace(const rkv_page_pool* pool, const rkv_paged_batch* batch, int q_heads, int n_rows,
                         int with_weight, long long* bytes);

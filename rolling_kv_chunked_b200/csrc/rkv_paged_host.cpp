@@ -17,6 +17,7 @@ namespace {
 
 constexpr int kMaxSeqs = 1 << 16;
 constexpr unsigned long long kWaitNs = 2000000000ull;  // cap on each device wait
+constexpr long long kMaxScores = 1LL << 32;  // bytes of scores that a call keeps at most (in its workspace)
 constexpr int kMaxGroup = 128;  // query heads of one KV head: one tile of query rows holds a token's
 
 bool aligned16(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -131,12 +132,16 @@ rkv::PagedPlan plan_of(const rkv_page_pool* pool, const rkv_paged_batch* b, int 
     if (weight && b->n_seqs <= rkv::kPagedMaxOrder) p.order = take(4LL * b->n_seqs);
   }
   p.score_stride = (b->max_kv + 63LL) / 64 * 64;
-  // scores are kept for at most 16 rows: 8 bytes of traffic for each, where reading K again takes 256
+  // Scores are kept for at most 16 rows (8 bytes of traffic for each, where reading K again takes 256 for all of them),
+  // but not past kMaxScores: their size goes by max_kv, which a captured step sets to the longest stream it may ever
+  // see. The weights are then formed from K again, as for more rows. The limit is high, since that takes longer: 64
+  // streams of 131072 tokens, 32 heads on 8 (1 GiB of scores), 5.8 ms with them and 13.7 without; of 4096 tokens,
+  // 257 and 471 us; 24 of 8192 tokens, 169 and 353 us.
   p.scores = -1;
   if (weight && p.slot_rows == 16) {
     if (p.score_stride > 0 && heads > (1LL << 48) / p.score_stride)
-      p.total = -1;  // no memory holds that, and the sum would pass 64 bits
-    else
+      p.total = -1;  // pairs of rows and places are counted in 48 bits
+    else if (4 * heads * p.score_stride <= kMaxScores)
       p.scores = take(4 * heads * p.score_stride);
   }
   return p;

@@ -830,3 +830,17 @@ def test_write_of_a_chunk_longer_than_its_stream(kvs, qs):
     assert torch.equal(c.k.view(torch.int16), want_k.view(torch.int16))
     assert torch.equal(c.v.view(torch.int16), want_v.view(torch.int16))
     assert c.batch.poll() == rkv.OK
+
+
+@pytest.mark.parametrize("hq,hk,qs,spare", [(16, 1, [1, 1], 5), (4, 4, [3, 16], 40), (3, 1, [5, 2], 300)])
+def test_weights_without_kept_scores(hq, hk, qs, spare):
+    """Host bounds for which the scores would pass what a call keeps: the weights come from K again, in a workspace of
+    ordinary size."""
+    bound = (1 << 30) // ((sum(qs) + spare) * hq) + 64
+    c = Cache(47, [700, 90], qs, hq, hk, 128, max_kv=bound, spare_rows=spare)
+    assert rkv.paged_workspace_bytes(c.pool, c.batch, c.rows + spare, hq, True) < 1 << 27
+    weight = torch.rand((2, hk, bound), device="cuda")
+    for causal in (True, False):
+        old = weight.clone()
+        out, z = c.attend(causal, weight=weight)
+        c.check(out, z, causal, weight, old)

@@ -117,3 +117,18 @@ def test_binding_refuses_tensors_that_do_not_fit():
     assert e.value.code == rkv.ERR_ARG
     with pytest.raises(rkv.RkvError):
         rkv.PagedBatch(torch.zeros(2, 4, dtype=torch.int32), torch.zeros(2, dtype=torch.int32), None, 1, 64)
+
+
+def test_workspace_of_kept_scores_is_bounded():
+    """Scores go by max_kv, up to 2^32 bytes; past that none are kept."""
+    def size(weight, kv, rows=8, max_q=8, heads=4):
+        n = ctypes.c_longlong(-1)
+        b = batch(max_q=max_q, table_stride=kv // 16, max_kv=kv)
+        assert rkv._lib.rkv_paged_workspace(pool(), b, heads, rows, weight, ctypes.byref(n)) == rkv.OK
+        return n.value
+
+    most = (1 << 32) // (4 * 8 * 4)
+    extra = [size(1, kv) - size(0, kv) for kv in (most, most + 64, 16 * most)]
+    assert extra[0] >= 1 << 32 and extra[0] < (1 << 32) + 1024
+    assert extra[1] == extra[2] < 1024
+    assert size(1, most, max_q=20) - size(0, most, max_q=20) < 1024  # more rows: never
