@@ -186,6 +186,13 @@ def _refuse(where: str):
     raise RkvError(ERR_ARG, where)
 
 
+def _int32(x, where: str) -> int:
+    """x as the library takes it; refused where a C int would keep the low 32 bits."""
+    if not -(1 << 31) <= x < 1 << 31:
+        _refuse(where)
+    return x
+
+
 def _dense(t, dtype, shape, index, where: str):
     """Pointer of a contiguous tensor of this type and shape (None: any extent) on GPU ``index``; refused otherwise."""
     if t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
@@ -274,7 +281,8 @@ class PagedBatch:
                 _dense(t, i32, shape, dev.index, where)
         self.page_table, self.kv_len, self.q_start, self.status = page_table, kv_len, q_start, status
         self.device, self.index, self.n_seqs, self.width, self.max_kv = dev, dev.index, n, width, max_kv
-        self._c = _PagedBatch(_ptr(page_table), _ptr(kv_len), _ptr(q_start), _ptr(status), stride, n, max_q, max_kv)
+        self._c = _PagedBatch(_ptr(page_table), _ptr(kv_len), _ptr(q_start), _ptr(status),
+                              _int32(stride, where), n, _int32(max_q, where), _int32(max_kv, where))
         self._ref = ctypes.byref(self._c)
 
     def poll(self, stream=None) -> int:
@@ -296,10 +304,11 @@ def paged_write(pool: PagePool, batch: PagedBatch, k, v, stream=None) -> None:
 
 def paged_workspace_bytes(pool: PagePool, batch: PagedBatch, rows: int, q_heads: int, weight: bool = False) -> int:
     """Bytes of workspace that ``paged_attention`` needs for a chunk tensor of ``rows`` rows."""
-    _pair(pool, batch, "rkv_paged_workspace")
+    where = "rkv_paged_workspace"
+    _pair(pool, batch, where)
     n = _c_ll(0)
-    _check(_lib.rkv_paged_workspace(pool._ref, batch._ref, q_heads, rows, int(bool(weight)), ctypes.byref(n)),
-           "rkv_paged_workspace")
+    _check(_lib.rkv_paged_workspace(pool._ref, batch._ref, _int32(q_heads, where), _int32(rows, where),
+                                    int(bool(weight)), ctypes.byref(n)), where)
     return n.value
 
 
@@ -347,8 +356,8 @@ def paged_evict(pool: PagePool, batch: PagedBatch, weight, keep: int, sinks: int
     wp = _dense(weight, torch.float32, (n, pool.kv_heads, None), index, where)
     kp = _dense(kept, torch.int32, (n, pool.kv_heads, keep), index, where)
     lp = _dense(kv_len_out, torch.int32, (n,), index, where)
-    _launch(_lib.rkv_paged_evict, where, pool, stream, pool._ref, batch._ref, wp, weight.shape[2], keep, sinks,
-            recent, kp, lp)
+    _launch(_lib.rkv_paged_evict, where, pool, stream, pool._ref, batch._ref, wp, weight.shape[2],
+            _int32(keep, where), _int32(sinks, where), _int32(recent, where), kp, lp)
 
 
 class RollingKV:

@@ -844,3 +844,20 @@ def test_weights_without_kept_scores(hq, hk, qs, spare):
         old = weight.clone()
         out, z = c.attend(causal, weight=weight)
         c.check(out, z, causal, weight, old)
+
+
+def test_host_numbers_past_31_bits_are_refused():
+    c = Cache(44, [200, 300], [1, 1], 4, 2, 16)
+    weight = torch.zeros((2, 2, 300), device="cuda")
+    kept = torch.empty((2, 2, 10), dtype=torch.int32, device="cuda")
+    for far in (1 << 31, (1 << 32) + 1, -(1 << 32)):
+        for call in (lambda: rkv.PagedBatch(c.table, c.kv_len, c.q_start, far, 300),
+                     lambda: rkv.PagedBatch(c.table, c.kv_len, c.q_start, 1, far),
+                     lambda: rkv.paged_evict(c.pool, c.batch, weight, 10, far, 1, kept, torch.empty_like(c.kv_len)),
+                     lambda: rkv.paged_evict(c.pool, c.batch, weight, 10, 1, far, kept, torch.empty_like(c.kv_len)),
+                     lambda: rkv.paged_workspace_bytes(c.pool, c.batch, far, 4),
+                     lambda: rkv.paged_workspace_bytes(c.pool, c.batch, 2, far)):
+            with pytest.raises(rkv.RkvError) as e:
+                call()
+            assert e.value.code in (rkv.ERR_ARG, rkv.ERR_UNSUPPORTED)
+    torch.cuda.synchronize()
