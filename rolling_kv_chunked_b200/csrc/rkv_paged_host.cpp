@@ -22,7 +22,12 @@ constexpr int kMaxGroup = 128;  // query heads of one KV head: one tile of query
 
 bool aligned16(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned4(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-int cuda_rc(cudaError_t e) { return e == cudaSuccess ? RKV_OK : RKV_ERR_CUDA; }
+// A failure is reported here and cleared: the rolling window's calls ask for the last error after their launches.
+int cuda_rc(cudaError_t e) {
+  if (e == cudaSuccess) return RKV_OK;
+  cudaGetLastError();
+  return RKV_ERR_CUDA;
+}
 
 // Host values of the pool and the batch (what rkv_paged_workspace looks at, no pointers).
 int check_sizes(const rkv_page_pool* pool, const rkv_paged_batch* b, int n_rows) {
@@ -302,9 +307,10 @@ RKV_API int rkv_paged_poll_status(unsigned* status, void* stream) {
   // all in the stream's order: a clear on another stream could wipe out what this one's next kernel reports
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   unsigned word = 0;
-  if (cudaMemcpyAsync(&word, status, sizeof(word), cudaMemcpyDeviceToHost, st) != cudaSuccess) return RKV_ERR_CUDA;
-  if (cudaStreamSynchronize(st) != cudaSuccess) return RKV_ERR_CUDA;
-  if (word != 0 && cudaMemsetAsync(status, 0, sizeof(word), st) != cudaSuccess) return RKV_ERR_CUDA;
+  cudaError_t err = cudaMemcpyAsync(&word, status, sizeof(word), cudaMemcpyDeviceToHost, st);
+  if (err == cudaSuccess) err = cudaStreamSynchronize(st);
+  if (err == cudaSuccess && word != 0) err = cudaMemsetAsync(status, 0, sizeof(word), st);
+  if (err != cudaSuccess) return cuda_rc(err);
   if (word & rkv::kStatusTimeout) return RKV_ERR_TIMEOUT;
   return (word & (rkv::kStatusPage | rkv::kStatusLength)) ? RKV_ERR_PAGE : RKV_OK;
 }

@@ -861,3 +861,21 @@ def test_host_numbers_past_31_bits_are_refused():
                 call()
             assert e.value.code in (rkv.ERR_ARG, rkv.ERR_UNSUPPORTED)
     torch.cuda.synchronize()
+
+
+def test_a_failed_call_leaves_no_error_for_the_next():
+    """A poll inside a capture is refused by CUDA; calls of the rolling window after it do not report that."""
+    import ctypes
+    rt = ctypes.CDLL("libcudart.so.12")
+    c = Cache(45, [200], [1], 4, 2, 16)
+    x = [torch.zeros(1024, dtype=torch.bfloat16, device="cuda") for _ in range(5)]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    st, graph = ctypes.c_void_p(side.cuda_stream), ctypes.c_void_p()
+    assert rt.cudaStreamBeginCapture(st, 1) == 0  # this thread's calls only
+    assert c.batch.poll(side) == rkv.ERR_CUDA
+    assert rt.cudaStreamEndCapture(st, ctypes.byref(graph)) != 0  # the poll has spoilt it
+    rt.cudaGetLastError()
+    rkv.flow_x0_renoise(*x[:3], 0.5, 0.25, x[3], x[4])
+    torch.cuda.synchronize()
+    assert c.batch.poll() == rkv.OK
