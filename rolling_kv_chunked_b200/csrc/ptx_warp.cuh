@@ -14,6 +14,12 @@ __device__ __forceinline__ void let_next_launch() { asm volatile("griddepcontrol
 // Wait until the previous kernel has completed and its writes are visible.
 __device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// ------------------------------------------------------------------ named barriers
+// Count this warp at hardware barrier `id` of `count` threads without waiting there (named_bar_sync waits).
+__device__ __forceinline__ void named_bar_arrive(int id, int count) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
+
 // ------------------------------------------------------------------ asynchronous 16-byte copies
 __device__ __forceinline__ void cp_async16(uint32_t dst_smem, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst_smem), "l"(src) : "memory");

@@ -27,6 +27,10 @@
 // bytes the tile holds there; V rows past the last visible token are left out of the product in
 // steps of 16 tokens, and zeroed within the last step, since 0 times a stale NaN would be NaN.
 // Every wait is bounded; on expiry the block reports, drains what it issued and returns.
+//
+// A wait names its phase by parity, so no barrier may complete a phase more than one ahead of any warp that waits
+// at it, however long that warp is held up. Nearly always the next phase needs something of every such warp; the
+// two waits that see to it elsewhere say so (tests/test_chunk_barriers.py models the protocol).
 #include <algorithm>
 #include <mutex>
 
@@ -635,6 +639,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok && (u.last_valid & 15)) {
         const int st = (nv - 1) & 1;
         ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars[kBarVFull + st], ((nv - 1) >> 1) & 1, limit));
+        // The value product before this tile's was issued, so the issuer has seen the kBarVFix of the unit before: of
+        // two phases completed in a row it would wait for the one that has the first one's parity again.
+        if (ok && nv >= 2)
+          ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars[kBarVEmpty + (st ^ 1)], ((nv - 2) >> 1) & 1, limit));
         if (ok) {
           const int end = (u.last_valid + 15) & ~15;
           for (int i = lane; i < (end - u.last_valid) * 16; i += 32)
@@ -764,6 +772,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int seen = min(u.k.keys, p.causal && live ? u.k.place0 + tile0 + tok + 1 : u.k.keys) - u.j0;
       const int n_mine = u.two ? u.n_tiles : (u.n_tiles + 1 - wg) >> 1;
       float m_used = kNoKey, l = 0.f, pend = 1.0f;
+      // A unit of one score tile takes nothing from the second warpgroup before its end: it may not complete kBarODone
+      // while a warp there still waits for that of the unit before, which has the other parity.
+      if (!u.two && u.n_tiles == 1) {
+        if (wg == 0)
+          ptx::named_bar_sync(2, 256);
+        else
+          ptx::named_bar_arrive(2, 256);
+      }
       for (int i = 0; i < n_mine; ++i, ++n_s) {
         if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait(&bars[kBarSFull + wg], n_s & 1, limit));
         if (!ok) continue;

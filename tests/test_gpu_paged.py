@@ -879,3 +879,21 @@ def test_a_failed_call_leaves_no_error_for_the_next():
     rkv.flow_x0_renoise(*x[:3], 0.5, 0.25, x[3], x[4])
     torch.cuda.synchronize()
     assert c.batch.poll() == rkv.OK
+
+
+def test_thousands_of_units_of_one_tile():
+    """Odd chunks of two query tiles and one, of one key tile each or none: 2000 units a call, again and again, every
+    wait answered and the same bits each time."""
+    kvs = [0, 1, 9, 14, 20, 18, 0, 11, 2, 16, 33, 128, 127, 100] * 3
+    qs = [1, 249, 9, 97, 20, 144, 287, 193, 41, 101, 33, 127, 3, 55] * 3
+    c = Cache(48, kvs, qs, 127, 1, 16, spare_rows=1)
+    old = torch.rand((len(kvs), 1, c.max_kv), device="cuda")
+    weight = old.clone()
+    first = c.attend(False, weight=weight)
+    c.check(*first, False, weight, old)
+    w = torch.empty_like(weight)
+    for _ in range(300):
+        w.copy_(old)
+        out, z = c.attend(False, weight=w)
+        assert torch.equal(out[:c.rows], first[0][:c.rows]) and torch.equal(w, weight)
+    assert c.batch.poll() == rkv.OK
