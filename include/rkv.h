@@ -356,7 +356,14 @@ int rkv_copy_heads(const rkv_head_copy* runs, int n_runs, int n_heads, void* str
  * outputs unwritten (a q_start that decreases somewhere: any stream's), a page id outside [0, n_pages) is never followed (its keys are read from
  * page 0, writes to it are dropped), and both set `status`, read by rkv_paged_poll_status.
  * Slots at and after kv_len may hold anything, NaN included; cached tokens before it have to
- * be finite.
+ * be finite, and scores (q . k / sqrt(128)) below 5e8 in magnitude: they are held in fp32.
+ *
+ * The bounds cost time where they are far above the lengths: max_q * (q_heads / kv_heads) up to
+ * 32 takes the kernels for few rows, and a larger one those for chunks, for every stream of the call, so
+ * a few chunks beside many single tokens are two calls (a batch may name a part of the lists and
+ * of q_start, over the same chunk tensors); max_kv sets the grid of the single-token weights and
+ * the workspace. Every thread block looks at the lengths of all streams, which
+ * shows from some hundreds of short streams on.
  */
 
 /* The pages of one layer. page_stride: bf16 elements from one page to the next, a multiple of
@@ -389,7 +396,8 @@ typedef struct {
  * rkv_paged_write - the chunk's K and V into the pages: row i of stream s to place
  *  kv_len[s] - n_q + i; a row whose place would be negative is left out. A bit copy. k, v: [n_rows, kv_heads, 128] bf16, 16-byte aligned,
  *  k_stride / v_stride elements from one row to the next (multiples of 8, at least
- *  kv_heads * 128). A page listed twice under the written places holds one of the two writes.
+ *  kv_heads * 128). Where a page is listed twice under the written places, every 16 bytes of it
+ *  are one of the two writes'.
  *  Errors: RKV_ERR_ARG, RKV_ERR_UNSUPPORTED, RKV_ERR_CUDA.
  */
 int rkv_paged_write(const rkv_page_pool* pool, const rkv_paged_batch* batch, const void* k, const void* v,
